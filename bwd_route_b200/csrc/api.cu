@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "checks.h"
 #include "hmean.h"
 #include "internal.h"
 #include "moe_top1.h"
@@ -18,7 +19,6 @@ cudaError_t tf32_set_smem_limits();
 
 namespace {
 
-constexpr int64_t kMaxT = (int64_t{1} << 31) - 256;
 constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
@@ -59,30 +59,6 @@ cudaError_t device_info(DeviceInfo** out) {
     return cudaSuccess;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Range {
-    const void* p;
-    size_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-// Every output must be disjoint from every other output and from every input.
-bool any_alias(const Range* outs, int n_out, const Range* ins, int n_in) {
-    for (int i = 0; i < n_out; ++i) {
-        for (int j = i + 1; j < n_out; ++j)
-            if (overlap(outs[i], outs[j])) return true;
-        for (int j = 0; j < n_in; ++j)
-            if (overlap(outs[i], ins[j])) return true;
-    }
-    return false;
-}
-
 moe_status_t tokens(int64_t B, int64_t N_H, int64_t* T) {
     if (B < 0 || N_H < 0) return MOE_ERR_INVALID_ARG;
     if (N_H != 0 && B > kMaxT / N_H) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -96,8 +72,6 @@ bool h_supported(int H, moe_math_t math) {
     if (math == MOE_MATH_FFMA) return H >= 32 && H <= 256 && H % 32 == 0;
     return false;
 }
-
-moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 EncodeTiledFn g_encode = nullptr;
 

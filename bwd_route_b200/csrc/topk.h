@@ -1,0 +1,18 @@
+// topk.h -- host-side declarations shared by the files of the top-k block.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "moe_topk.h"
+
+namespace moe {
+
+inline bool dtype_ok(moe_dtype_t d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
+inline size_t dtype_bytes(moe_dtype_t d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
+
+// SMs of the current device.
+cudaError_t device_sms(int* out);
+
+}  // namespace moe

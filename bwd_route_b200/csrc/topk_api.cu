@@ -1,0 +1,32 @@
+// topk_api.cu -- what the files of the top-k block (include/moe_topk.h) share: the
+// ABI version and the facts about the current device.
+#include <mutex>
+
+#include "topk.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxDevices = 64;
+int g_sms[kMaxDevices];
+std::mutex g_mu;
+
+}  // namespace
+
+cudaError_t device_sms(int* out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (g_sms[dev] == 0) {
+        e = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+    }
+    *out = g_sms[dev];
+    return cudaSuccess;
+}
+
+}  // namespace moe
+
+extern "C" int32_t moe_topk_abi_version(void) { return MOE_TOPK_ABI_VERSION; }

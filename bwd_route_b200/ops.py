@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libmoe_top1.so (C ABI: include/moe_top1.h).
+"""Thin ctypes binding of libmoe_top1.so (C ABI: include/moe_top1.h for the top-1
+gate, include/moe_topk.h for the top-k block).
 
 Argument marshalling only: every function takes torch tensors that already
 live on the GPU, checks their dtype / contiguity, and passes data pointers and
@@ -35,6 +36,11 @@ EXPORTED = [
     "moe_top1_check_routing", "moe_aux_loss_fwd_bwd_lambda_update",
 ]
 MOE_NOALLOC_MAX_TOKENS = 2097152
+
+# The top-k block (include/moe_topk.h).
+MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
+_DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+EXPORTED_TOPK = ["moe_topk_abi_version", "moe_layer_norm_fwd", "moe_layer_norm_workspace_bytes", "moe_layer_norm_bwd"]
 
 
 class MoeError(RuntimeError):
@@ -101,6 +107,15 @@ def lib() -> ctypes.CDLL:
         L.moe_top1_check_routing.argtypes = [ctypes.POINTER(RoutingC), I64, I32, P, SZ, P]
         L.moe_top1_route_noalloc.restype = I32
         L.moe_top1_route_noalloc.argtypes = [P, I64, I64, I32, ctypes.POINTER(RoutingC), P]
+        L.moe_topk_abi_version.restype = I32
+        L.moe_topk_abi_version.argtypes = []
+        F = ctypes.c_float
+        L.moe_layer_norm_fwd.restype = I32
+        L.moe_layer_norm_fwd.argtypes = [P, I32, I64, I32, I64, P, P, I32, F, P, P, P, P]
+        L.moe_layer_norm_workspace_bytes.restype = SZ
+        L.moe_layer_norm_workspace_bytes.argtypes = [I64, I32]
+        L.moe_layer_norm_bwd.restype = I32
+        L.moe_layer_norm_bwd.argtypes = [P, P, I32, I64, I32, I64, P, I32, P, P, P, P, P, P, SZ, P]
         _lib = L
     return _lib
 
@@ -284,3 +299,88 @@ def moe_top1_device_flags(ws: torch.Tensor, stream=None) -> int:
     if st not in (0, 7):
         raise MoeError("moe_top1_device_flags", st)
     return int(flags.value)
+
+
+# ---------------------------------------------------------------- top-k block
+def _arg(name: str, t: torch.Tensor | None, dev: int, dtype, *shape):
+    """Address of a dense tensor of this type and shape on device dev, or None."""
+    if t is None:
+        return None
+    if t.device.index != dev or not t.is_cuda:
+        raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows(name: str, t: torch.Tensor):
+    """(device, dtype, rows, columns, row stride) of a [T, H] tensor with dense rows
+    on the current device, the one whose stream the call is enqueued on."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device, got {t.device}")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a [T, H] tensor, got shape {tuple(t.shape)}")
+    T, H = t.shape
+    if H > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: expected rows of adjacent elements")
+    ld = t.stride(0) if T > 1 else H
+    if ld < H:
+        raise ValueError(f"{name}: expected rows that do not overlap")
+    return t.device.index, t.dtype, T, H, ld
+
+
+def _workspace(ws: torch.Tensor | None, dev: int):
+    if ws is None:
+        return None, 0
+    return _arg("ws", ws, dev, torch.uint8, ws.numel()), ws.numel()
+
+
+def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().moe_layer_norm_workspace_bytes(T, H))
+
+
+def new_layer_norm_workspace(T: int, H: int, device, stream=None) -> torch.Tensor:
+    """Allocates (torch) and initialises a workspace for moe_layer_norm_bwd on [T, H]."""
+    ws = torch.empty(max(moe_layer_norm_workspace_bytes(T, H), 256), dtype=torch.uint8, device=device)
+    moe_top1_workspace_init(ws, stream)
+    return ws
+
+
+def _param_dtype(name: str, dtype, *params):
+    """Type of the parameters: that of the ones given, which have to agree."""
+    kinds = {p.dtype for p in params if p is not None} or {dtype}
+    if len(kinds) > 1 or not kinds <= {dtype, torch.float32}:
+        raise TypeError(f"{name}: expected parameters of one type, {dtype} or float32, got {sorted(map(str, kinds))}")
+    return kinds.pop()
+
+
+def moe_layer_norm_fwd(x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None):
+    """y = (x - mean) * rstd * gamma + beta over the last axis of x [T, H] (rows may be
+    strided). gamma and beta [H] may be None; mean and rstd [T] are kept for the backward."""
+    dev, dt, T, H, ld = _rows("x", x)
+    pd = _param_dtype("gamma, beta", dt, gamma, beta)
+    f = torch.float32
+    _check("moe_layer_norm_fwd",
+           lib().moe_layer_norm_fwd(x.data_ptr(), _DTYPES[dt], T, H, ld, _arg("gamma", gamma, dev, pd, H),
+                                    _arg("beta", beta, dev, pd, H), _DTYPES[pd], eps, _arg("y", y, dev, dt, T, H),
+                                    _arg("mean", mean, dev, f, T), _arg("rstd", rstd, dev, f, T), _stream(stream)))
+
+
+def moe_layer_norm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
+    """Gradients of moe_layer_norm_fwd; dx, dgamma and dbeta are written where given."""
+    dev, dt, T, H, ld = _rows("x", x)
+    pd = _param_dtype("gamma, dgamma, dbeta", dt, gamma, dgamma, dbeta)
+    f = torch.float32
+    w, n = _workspace(ws, dev)
+    _check("moe_layer_norm_bwd",
+           lib().moe_layer_norm_bwd(x.data_ptr(), _arg("dy", dy, dev, dt, T, H), _DTYPES[dt], T, H, ld,
+                                    _arg("gamma", gamma, dev, pd, H), _DTYPES[pd], _arg("mean", mean, dev, f, T),
+                                    _arg("rstd", rstd, dev, f, T), _arg("dx", dx, dev, dt, T, H),
+                                    _arg("dgamma", dgamma, dev, pd, H), _arg("dbeta", dbeta, dev, pd, H), w, n,
+                                    _stream(stream)))

@@ -1,0 +1,93 @@
+"""Host-side checks of the top-k block's C ABI (include/moe_topk.h), without a GPU:
+what the header declares is exported and bound, and bad arguments are refused with
+the documented status before anything touches the GPU."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from bwd_route_b200 import build as libbuild
+from bwd_route_b200 import ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "moe_topk.h")
+
+OK, INVALID, SHAPE, MISALIGNED, ALIAS, WORKSPACE = 0, 1, 2, 3, 4, 5
+F32, BF16, F16 = 0, 1, 2
+
+# Fake device addresses, 16 MiB apart: the checks compare and align them only.
+A = [0x7F0000000000 + (i << 24) for i in range(32)]
+
+
+@pytest.fixture(scope="module")
+def L():
+    libbuild.build()
+    return ops.lib()
+
+
+def test_every_declared_symbol_is_exported_and_bound(L):
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    fns = sorted(set(re.findall(r"^\s*(?:const\s+)?\w+\**\s+\**(moe_\w+)\s*\(", text, flags=re.M)))
+    assert fns == sorted(ops.EXPORTED_TOPK)
+    for name in fns:
+        assert hasattr(L, name) and getattr(L, name).argtypes is not None, name
+    version = int(re.search(r"#define MOE_TOPK_ABI_VERSION (\d+)", text).group(1))
+    assert L.moe_topk_abi_version() == version
+
+
+def norm_fwd(L, **k):
+    v = dict(x=A[0], dtype=BF16, T=10, H=64, ldx=64, gamma=A[1], beta=A[2], pd=BF16, eps=1e-5, y=A[3], mean=A[4],
+             rstd=A[5])
+    v.update(k)
+    return L.moe_layer_norm_fwd(v["x"], v["dtype"], v["T"], v["H"], v["ldx"], v["gamma"], v["beta"], v["pd"], v["eps"],
+                                v["y"], v["mean"], v["rstd"], None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(ldx=63), INVALID), (dict(dtype=3), INVALID),
+    (dict(pd=F16), INVALID), (dict(pd=-1), INVALID), (dict(eps=-1e-5), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(eps=float("inf")), INVALID), (dict(x=None), INVALID), (dict(y=None), INVALID),
+    (dict(T=2 ** 31 - 256), SHAPE), (dict(H=8193, ldx=8193), SHAPE), (dict(ldx=2 ** 31 + 1), SHAPE),
+    (dict(x=A[0] + 1), MISALIGNED), (dict(y=A[3] + 1), MISALIGNED), (dict(gamma=A[1] + 1), MISALIGNED),
+    (dict(mean=A[4] + 2), MISALIGNED), (dict(rstd=A[5] + 2), MISALIGNED),
+    (dict(pd=F32, gamma=A[1] + 2), MISALIGNED),
+    (dict(y=A[0] + 2), ALIAS), (dict(y=A[0], ldx=80), ALIAS), (dict(y=A[1] - 20), ALIAS), (dict(mean=A[0] + 128), ALIAS),
+    (dict(rstd=A[4] + 36), ALIAS), (dict(mean=A[3] + 10 * 128 - 4), ALIAS), (dict(beta=A[3] + 2), ALIAS),
+    (dict(T=0), OK), (dict(T=0, x=None, y=None), OK),
+])
+def test_layer_norm_fwd_refuses(L, change, status):
+    assert norm_fwd(L, **change) == status
+
+
+def norm_bwd(L, **k):
+    v = dict(x=A[0], dy=A[1], dtype=BF16, T=10, H=64, ldx=64, gamma=A[2], pd=BF16, mean=A[3], rstd=A[4], dx=A[5],
+             dg=A[6], db=A[7], ws=A[8], n=1 << 20)
+    v.update(k)
+    return L.moe_layer_norm_bwd(v["x"], v["dy"], v["dtype"], v["T"], v["H"], v["ldx"], v["gamma"], v["pd"], v["mean"],
+                                v["rstd"], v["dx"], v["dg"], v["db"], v["ws"], v["n"], None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=-1), INVALID), (dict(ldx=10), INVALID), (dict(dtype=7), INVALID), (dict(pd=F16), INVALID),
+    (dict(x=None), INVALID), (dict(dy=None), INVALID), (dict(mean=None), INVALID), (dict(rstd=None), INVALID),
+    (dict(H=9000, ldx=9000), SHAPE), (dict(dx=A[5] + 1), MISALIGNED), (dict(dg=A[6] + 1), MISALIGNED),
+    (dict(ws=A[8] + 16), MISALIGNED), (dict(ws=None), WORKSPACE), (dict(n=256), WORKSPACE),
+    (dict(dx=A[1] + 2), ALIAS), (dict(dx=A[0]), ALIAS), (dict(dg=A[7] + 126), ALIAS), (dict(dg=A[1], dx=A[1]), ALIAS),
+    (dict(ws=A[1]), ALIAS), (dict(db=A[8] + 512), ALIAS), (dict(mean=A[8] + 512), ALIAS),
+    (dict(dx=None, dg=None, db=None), OK),
+])
+def test_layer_norm_bwd_refuses(L, change, status):
+    assert norm_bwd(L, **change) == status
+
+
+def test_layer_norm_workspace_bytes(L):
+    f = L.moe_layer_norm_workspace_bytes
+    assert f(0, 64) == 256 and f(1, 64) == 256 + 512 and f(10 ** 6, 64) == 256 + 1024 * 512
+    assert f(-1, 64) == 0 and f(5, 0) == 0 and f(5, 8193) == 0 and f(2 ** 31, 64) == 0
+
+
+def test_binding_refuses_tensors_it_cannot_pass():
+    with pytest.raises(ValueError):
+        ops.moe_layer_norm_fwd(torch.zeros(2, 4), None, None, 1e-5, torch.zeros(2, 4))
