@@ -15,4 +15,7 @@ inline size_t dtype_bytes(moe_dtype_t d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
 // SMs of the current device.
 cudaError_t device_sms(int* out);
 
+// Workspace of the router: the reserved head, then per-block counts and bases.
+size_t topk_route_ws_bytes(int64_t T, int E);
+
 }  // namespace moe

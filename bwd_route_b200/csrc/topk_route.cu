@@ -1,0 +1,850 @@
+// topk_route.cu -- the router of the top-k block: K experts per token with their
+// weights, the lists that group the T * K pairs by expert, and the gradient of the
+// logits.
+//
+//   s = softmax(l) or sigmoid(l);  v = s + bias;  masked (l = -inf or NaN): v = -inf
+//   groups: the top_groups groups with the largest sum of their `best` largest v stay
+//   the K largest v that stay, largest first, equal ones by index;  w = scale * s
+//   (renormalised: scale * s / sum of the chosen s, taken as a ratio of exponentials,
+//   so that it is finite where every s underflows)
+//
+// Choices are exact. Without a bias the order of v is that of the logits, which are
+// compared as they are. With a bias (or sums of scores per group) v is computed in
+// fp32, and where two neighbours in the result lie within the error of that
+// computation the warp repeats the choice in fp64; about 1 % of the warps do.
+//
+// A token belongs to LPT lanes with VPL consecutive experts each, so a warp works on
+// 32 / LPT tokens at once: K rounds of a local maximum, a shuffle maximum over the
+// lanes and a ballot, whose lowest lane holds the lowest index. The block counts its
+// pairs per expert in shared memory; a second kernel turns the blocks' counts into
+// each block's base positions, a third writes the lists (stable, as in route.cu).
+// Few tokens take one launch of one block that does all three.
+#include <cmath>
+#include <cstdint>
+
+#include "checks.h"
+#include "common.cuh"
+#include "elem.cuh"
+#include "internal.h"
+#include "moe_topk.h"
+#include "topk.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxE = 256, kMaxK = 16, kMaxGroups = 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSmallThreads = 1024;
+constexpr int kMaxBlocks = 1024;      // rows of per-block counts the workspace holds
+constexpr int kSmallPairs = 8192;     // pairs the one-block kernel keeps in shared memory
+constexpr unsigned kFull = 0xffffffffu;
+
+struct Rule {
+    int E, K, G, S, top_groups, best;  // S: experts per group
+    int sigmoid, renorm;
+    float scale;
+};
+
+// ---------------------------------------------------------------- keys
+// Unsigned integers in the order of the values (-0 counts as +0). 0: not a candidate;
+// 1: a masked expert; both below the key of every number.
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t key_of(double v) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return (b >> 63) ? ~b : (b | (1ull << 63));
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+template <typename V>
+struct KeyOf;
+template <>
+struct KeyOf<float> {
+    using type = uint32_t;
+};
+template <>
+struct KeyOf<double> {
+    using type = uint64_t;
+};
+
+__device__ __forceinline__ float exp_v(float x) { return expf(x); }
+__device__ __forceinline__ double exp_v(double x) { return exp(x); }
+// Only compared (fp32): an absolute error of 7 * 2^-24 is inside the border test. The
+// fast exponential is off by 2 + 1.173 |l| units in the last place at most, which times
+// s (1 - s) stays below 1.3 * 2^-24; the sum adds 1 and the division 4.
+__device__ __forceinline__ float sigmoid_v(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
+__device__ __forceinline__ double sigmoid_v(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+template <int LPT, typename V>
+__device__ __forceinline__ V lanes_max(V v) {
+#pragma unroll
+    for (int off = LPT / 2; off >= 1; off >>= 1) {
+        const V o = __shfl_xor_sync(kFull, v, off);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+template <int LPT, typename V>
+__device__ __forceinline__ V lanes_sum(V v) {
+#pragma unroll
+    for (int off = LPT / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    return v;
+}
+
+// ---------------------------------------------------------------- one token's row
+template <typename T, int VPL>
+__device__ __forceinline__ void load_logits(const T* row, int e0, int E, bool vec, bool valid, float (&l)[VPL]) {
+    constexpr int C = 16 / sizeof(T);
+    static_assert(VPL % C == 0, "whole chunks");
+    if (vec) {
+#pragma unroll
+        for (int j = 0; j < VPL; j += C) {
+            Chunk<T, C> c;
+            const bool on = valid && e0 + j < E;
+            if (on) c = *reinterpret_cast<const Chunk<T, C>*>(row + e0 + j);
+#pragma unroll
+            for (int i = 0; i < C; ++i) l[j + i] = on ? to_f(c.v[i]) : 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) l[j] = (valid && e0 + j < E) ? to_f(row[e0 + j]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ bool is_masked(float l) { return !(l > -INFINITY); }
+
+// Maximum and sum of exponentials of a softmax row over its lanes (fp32 or fp64). A row
+// of nothing but -inf gives m = 0, z = 1 (every score is then exp(-inf) = 0).
+template <typename V, int LPT, int VPL>
+__device__ __forceinline__ void softmax_stats(const float (&l)[VPL], int e0, int E, V& m, V& z) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+        if (e0 + j < E && l[j] > mx) mx = l[j];
+    mx = lanes_max<LPT>(mx);
+    if (mx == -INFINITY) mx = 0.0f;
+    V s = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+        if (e0 + j < E) s += exp_v(static_cast<V>(l[j]) - static_cast<V>(mx));
+    s = lanes_sum<LPT>(s);
+    m = mx;
+    z = s == V(0) ? V(1) : s;
+}
+
+// Shared memory of one warp: per token of the warp K + 1 chosen experts and their keys'
+// values, and with groups the values and the group scores.
+template <typename V>
+struct WarpSmem {
+    int* slot;    // [32 / LPT][K + 1]
+    float* slot_v;
+    V* val;       // [32 / LPT][E padded], group selection only
+    V* gscore;    // [32 / LPT][G]
+};
+
+__device__ __forceinline__ int pad_e(int e) { return e + (e >> 5); }
+__host__ __device__ constexpr int padded(int ep) { return ep + ep / 32 + 1; }
+
+// Chooses the experts of the warp's tokens: slot[k] of each. V = float: returns whether a
+// choice lies too near a border to be certain (true for some lane of the token).
+// SCORES: some order needs the scores (a bias, or group sums).
+template <typename V, typename T, int LPT, int VPL, bool SCORES>
+__device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, const float* __restrict__ bias,
+                                       const Rule& R, const WarpSmem<V>& sm) {
+    using Key = typename KeyOf<V>::type;
+    constexpr bool kFast = sizeof(V) == 4;
+    const int lane = threadIdx.x & 31, sub = lane % LPT, tok = lane / LPT, g0 = tok * LPT, e0 = sub * VPL;
+    constexpr unsigned kMine = LPT == 32 ? kFull : (1u << (LPT & 31)) - 1u;
+    V m = 0, z = 1;
+    if (SCORES && !R.sigmoid) softmax_stats<V, LPT, VPL>(l, e0, R.E, m, z);
+    const V inv_z = V(1) / z;
+    auto score = [&](float x) -> V {
+        return R.sigmoid ? sigmoid_v(static_cast<V>(x)) : exp_v(static_cast<V>(x) - m) * inv_z;
+    };
+    Key key[VPL];
+    V v[VPL];  // what groups are scored by
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        const int e = e0 + j;
+        V order;
+        if (SCORES) {
+            v[j] = score(l[j]);
+            if (bias && e < R.E) v[j] += static_cast<V>(bias[e]);
+            order = bias ? v[j] : static_cast<V>(l[j]);
+        } else {
+            v[j] = order = static_cast<V>(l[j]);
+        }
+        const bool off = is_masked(l[j]) || order != order;
+        if (off) v[j] = -INFINITY;
+        key[j] = e >= R.E ? Key(0) : off ? Key(1) : key_of(order);
+    }
+    bool unsure = false;
+    // border of two values in fp32; see sigmoid_v. The softmax adds the error of its sum:
+    // 17 + 21 units for 256 terms.
+    const float tol = R.sigmoid ? 0x1p-20f : 0x1p-17f;
+    if (R.G > 1) {
+        V* val = sm.val + tok * padded(LPT * VPL);
+        V* gs = sm.gscore + tok * R.G;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) val[pad_e(e0 + j)] = v[j];
+        __syncwarp();
+        for (int g = sub; g < R.G; g += LPT) {
+            V a = -INFINITY, b = -INFINITY;
+            for (int i = 0; i < R.S; ++i) {
+                const V x = val[pad_e(g * R.S + i)];
+                if (x > a) {
+                    b = a;
+                    a = x;
+                } else if (x > b) {
+                    b = x;
+                }
+            }
+            gs[g] = R.best == 2 ? a + b : a;
+        }
+        __syncwarp();
+        unsigned kept = 0;
+        for (int i = 0; i < R.G; i += LPT) {
+            const int g = i + sub;
+            bool keep = false;
+            if (g < R.G) {
+                const V mine = gs[g];
+                int rank = 0;
+                for (int o = 0; o < R.G; ++o) {
+                    const V x = gs[o];
+                    rank += (x > mine || (x == mine && o < g)) ? 1 : 0;
+                }
+                keep = rank < R.top_groups;
+                if (kFast && SCORES) {
+                    // sums of two are off by up to twice as much
+                    const float t2 = 2.0f * tol * (1.0f + fabsf(static_cast<float>(mine)));
+                    int above = 0, near = 0;
+                    for (int o = 0; o < R.G; ++o) {
+                        const float d = static_cast<float>(gs[o]) - static_cast<float>(mine);
+                        above += d > t2 ? 1 : 0;
+                        near += (o != g && fabsf(d) <= t2) ? 1 : 0;
+                    }
+                    // a kept group that could fall out, or a dropped one that could come in
+                    unsure |= near > 0 && above < R.top_groups && above + near >= R.top_groups;
+                }
+            }
+            const unsigned b = __ballot_sync(kFull, keep);
+            kept |= ((b >> g0) & kMine) << i;
+        }
+        unsigned alive = 0;
+        for (int g = e0 / R.S; g < R.G && g * R.S < e0 + VPL; ++g) {
+            if (!((kept >> g) & 1u)) continue;
+            const int lo = max(g * R.S - e0, 0), hi = min((g + 1) * R.S - e0, VPL);
+            alive |= ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+        }
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (!((alive >> j) & 1u)) key[j] = 0;
+    }
+    constexpr bool kCheck = kFast && SCORES;
+    int* slot = sm.slot + tok * (R.K + 1);
+    float* slot_v = sm.slot_v + tok * (R.K + 1);
+    const int rounds = (kCheck && bias) ? R.K + 1 : R.K;
+    for (int k = 0; k < rounds; ++k) {
+        Key best = 0;
+        int at = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (key[j] > best) {
+                best = key[j];
+                at = j;
+            }
+        const Key top = lanes_max<LPT>(best);
+        const unsigned b = (__ballot_sync(kFull, best == top && top != 0) >> g0) & kMine;
+        const bool win = b != 0 && sub == __ffs(b) - 1;
+        if (win) {
+            slot[k] = e0 + at;
+            if constexpr (kCheck) slot_v[k] = top == 1 ? -INFINITY : value_of(static_cast<uint32_t>(top));
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (j == at) key[j] = 0;
+        } else if (b == 0 && sub == 0) {
+            slot[k] = -1;
+        }
+    }
+    __syncwarp();
+    if (kCheck && bias) {
+        for (int k = sub; k < R.K; k += LPT) {
+            const int ea = slot[k], eb = slot[k + 1];
+            if (eb < 0) continue;
+            const float a = slot_v[k], b = slot_v[k + 1];
+            // equal logits and equal biases are a true tie, in index order already
+            if (a - b <= tol * (1.0f + fabsf(a)) && !(to_f(row[ea]) == to_f(row[eb]) && bias[ea] == bias[eb])) unsure = true;
+        }
+    }
+    return unsure;
+}
+
+// The same in fp64, out of line: it is rare and would cost the others registers.
+template <typename T, int LPT, int VPL>
+__device__ __noinline__ void choose_exactly(const T* row, bool vec, bool valid, const float* __restrict__ bias, Rule R,
+                                            int* slot, double* val) {
+    float l[VPL];
+    load_logits<T, VPL>(row, (threadIdx.x % LPT) * VPL, R.E, vec, valid, l);
+    WarpSmem<double> sm{slot, nullptr, val, val + (32 / LPT) * padded(LPT * VPL)};
+    choose<double, T, LPT, VPL, true>(l, row, bias, R, sm);
+}
+
+// Bytes of one warp's area: slots, and (8-byte elements) group values and scores.
+__host__ __device__ inline int warp_bytes(const Rule& R, int lpt, int vpl) {
+    const int tpw = 32 / lpt;
+    int b = (tpw * (R.K + 1) * 8 + 7) / 8 * 8;
+    if (R.G > 1) b += tpw * (padded(lpt * vpl) + R.G) * 8;
+    return b;
+}
+
+// Routes the warp's tokens t (one per lane group; valid: t < T): writes expert_idx and
+// weights, adds to the block's histogram. s_idx: the pairs' experts kept for the
+// one-block kernel, or NULL.
+template <typename T, int LPT, int VPL, bool SCORES>
+__device__ __forceinline__ void route_tokens(const T* logits, int64_t ld, int64_t t, bool valid, bool vec,
+                                             const float* __restrict__ bias, const Rule& R, uint8_t* area, int* hist,
+                                             int32_t* __restrict__ expert_idx, float* __restrict__ weights, int* s_idx) {
+    constexpr int TPW = 32 / LPT;
+    const int lane = threadIdx.x & 31, sub = lane % LPT, tok = lane / LPT, e0 = sub * VPL;
+    const T* row = logits + (valid ? t : 0) * ld;
+    float l[VPL];
+    load_logits<T, VPL>(row, e0, R.E, vec, valid, l);
+    int* slots = reinterpret_cast<int*>(area);
+    double* wide = reinterpret_cast<double*>(area + (TPW * (R.K + 1) * 8 + 7) / 8 * 8);
+    float* narrow = reinterpret_cast<float*>(wide);
+    WarpSmem<float> sm{slots, reinterpret_cast<float*>(slots + TPW * (R.K + 1)), narrow,
+                       narrow + TPW * padded(LPT * VPL)};
+    const bool unsure = choose<float, T, LPT, VPL, SCORES>(l, row, bias, R, sm);
+    if (SCORES && __any_sync(kFull, unsure && valid))
+        choose_exactly<T, LPT, VPL>(row, vec, valid, bias, R, slots, wide);
+    float m = 0.0f, z = 1.0f;
+    if (!R.sigmoid && !R.renorm) softmax_stats<float, LPT, VPL>(l, e0, R.E, m, z);
+    const int* slot = slots + tok * (R.K + 1);
+    if (R.renorm) {
+        // ratios: the largest chosen exponent is 0
+        float mx = -INFINITY;
+        for (int k = sub; k < R.K; k += LPT) {
+            const float x = to_f(row[slot[k]]);
+            mx = fmaxf(mx, R.sigmoid ? fminf(x, 0.0f) : x);
+        }
+        mx = lanes_max<LPT>(mx);
+        if (mx == -INFINITY) mx = 0.0f;
+        m = mx;
+        float s = 0.0f;
+        for (int k = sub; k < R.K; k += LPT) {
+            const float x = to_f(row[slot[k]]);
+            const float p = expf((R.sigmoid && x >= 0.0f ? 0.0f : x) - m);
+            s += R.sigmoid ? p / (1.0f + expf(-fabsf(x))) : p;
+        }
+        s = lanes_sum<LPT>(s);
+        z = s == 0.0f ? 1.0f : s;
+    }
+    for (int k = sub; k < R.K; k += LPT) {
+        const int e = slot[k];
+        const float x = to_f(row[e]);
+        const float p = expf((R.sigmoid && x >= 0.0f ? 0.0f : x) - m);  // m = 0 for the plain sigmoid
+        const float w = (R.sigmoid ? p / (1.0f + expf(-fabsf(x))) : p) / z;
+        if (valid) {
+            expert_idx[t * R.K + k] = e;
+            weights[t * R.K + k] = R.scale * w;
+            atomicAdd(&hist[e], 1);
+            if (s_idx) s_idx[t * R.K + k] = e;
+        }
+    }
+    __syncwarp();
+}
+
+// Exclusive sums of n <= 256 values (one per thread of the first 256; others pass 0).
+__device__ __forceinline__ int exclusive_scan_256(int v, int* s_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(kFull, incl, off);
+        if (lane >= off) incl += u;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp && w < 8; ++w) before += s_warp[w];
+    __syncthreads();
+    return before + incl - v;
+}
+
+// Writes perm for the n pairs idx[0..n) whose first pair has number p0: the next position
+// of expert e is s_base[e]. s_pos: [warps][E]. Pairs of one expert stay in order: a warp
+// has a run of consecutive pairs, lanes of one expert are ranked by __match_any_sync.
+template <int WARPS>
+__device__ __forceinline__ void scatter_pairs(const int* idx, int n, int32_t p0, int E, const int* s_base, int* s_pos,
+                                              int32_t* __restrict__ perm) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = ((n + WARPS - 1) / WARPS + 31) & ~31;
+    const int lo = min(n, warp * run), hi = min(n, lo + run);
+    int* pos = s_pos + warp * E;
+    for (int e = lane; e < E; e += 32) pos[e] = 0;
+    __syncwarp();
+    const unsigned below = (1u << lane) - 1u;
+    for (int i = lo; i < hi; i += 32) {
+        const int e = i + lane < hi ? idx[i + lane] : -1;
+        const unsigned same = __match_any_sync(kFull, e);
+        if (e >= 0 && (same & below) == 0) pos[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += WARPS * 32) {
+        int at = s_base[e];
+        for (int w = 0; w < WARPS; ++w) {
+            const int c = s_pos[w * E + e];
+            s_pos[w * E + e] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int i = lo; i < hi; i += 32) {
+        const int e = i + lane < hi ? idx[i + lane] : -1;
+        const unsigned same = __match_any_sync(kFull, e);
+        const int at = e >= 0 ? pos[e] : 0;
+        if (e >= 0) perm[at + __popc(same & below)] = p0 + i + lane;
+        __syncwarp();
+        if (e >= 0 && (same & below) == 0) pos[e] = at + __popc(same);
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------- kernels
+// Tokens [b * tpb, (b + 1) * tpb) of block b; blk_counts [gridDim.x][E].
+template <typename T, int LPT, int VPL, bool SCORES>
+__global__ void __launch_bounds__(kThreads)
+topk_route_kernel(const T* __restrict__ logits, int64_t ld, int64_t T_, int tpb, bool vec,
+                  const float* __restrict__ bias, Rule R, int32_t* __restrict__ expert_idx,
+                  float* __restrict__ weights, int32_t* __restrict__ blk_counts) {
+    griddep_wait();  // every global access below comes after the previous grid
+    extern __shared__ __align__(16) uint8_t smem[];
+    int* hist = reinterpret_cast<int*>(smem);
+    const int warp = threadIdx.x >> 5, tok = (threadIdx.x & 31) / LPT;
+    uint8_t* area = smem + kMaxE * 4 + warp * warp_bytes(R, LPT, VPL);
+    constexpr int TPW = 32 / LPT;
+    for (int e = threadIdx.x; e < R.E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpb;
+    const int64_t t1 = t0 + tpb < T_ ? t0 + tpb : T_;
+    for (int64_t t = t0 + warp * TPW; t < t1; t += kWarps * TPW)
+        route_tokens<T, LPT, VPL, SCORES>(logits, ld, t + tok, t + tok < t1, vec, bias, R, area, hist, expert_idx,
+                                          weights, nullptr);
+    __syncthreads();
+    for (int e = threadIdx.x; e < R.E; e += kThreads) blk_counts[static_cast<int64_t>(blockIdx.x) * R.E + e] = hist[e];
+}
+
+// One block: routes every token, then counts, offsets and perm.
+template <typename T, int LPT, int VPL, bool SCORES>
+__global__ void __launch_bounds__(kSmallThreads)
+topk_route_small_kernel(const T* __restrict__ logits, int64_t ld, int T_, bool vec, const float* __restrict__ bias,
+                        Rule R, int32_t* __restrict__ expert_idx, float* __restrict__ weights,
+                        int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ perm) {
+    griddep_wait();  // every global access below comes after the previous grid
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_warp[32];
+    __shared__ int s_base[kMaxE];
+    constexpr int TPW = 32 / LPT, WARPS = kSmallThreads / 32;
+    int* hist = reinterpret_cast<int*>(smem);
+    int* s_idx = hist + kMaxE;                                       // [T * K]
+    uint8_t* areas = reinterpret_cast<uint8_t*>(s_idx + (T_ * R.K + 3) / 4 * 4);  // slots, then scatter positions
+    const int warp = threadIdx.x >> 5, tok = (threadIdx.x & 31) / LPT;
+    for (int e = threadIdx.x; e < R.E; e += kSmallThreads) hist[e] = 0;
+    __syncthreads();
+    for (int t = warp * TPW; t < T_; t += WARPS * TPW)
+        route_tokens<T, LPT, VPL, SCORES>(logits, ld, t + tok, t + tok < T_, vec, bias, R,
+                                          areas + warp * warp_bytes(R, LPT, VPL), hist, expert_idx, weights, s_idx);
+    __syncthreads();
+    const int e = threadIdx.x;
+    const int c = e < R.E ? hist[e] : 0;
+    const int off = exclusive_scan_256(c, s_warp);
+    if (e < R.E) {
+        counts[e] = c;
+        offsets[e] = off;
+        s_base[e] = off;
+    }
+    if (e == 0) offsets[R.E] = T_ * R.K;
+    __syncthreads();
+    scatter_pairs<WARPS>(s_idx, T_ * R.K, 0, R.E, s_base, reinterpret_cast<int*>(areas), perm);
+}
+
+// 32 experts a block (a lane each), the routing blocks in 32 runs (a warp each): sums of
+// the runs, then every block's base inside its expert and the expert's count.
+__global__ void __launch_bounds__(1024) topk_scan_kernel(const int32_t* __restrict__ blk_counts, int nblk, int E,
+                                                         int32_t* __restrict__ blk_base, int32_t* __restrict__ counts) {
+    griddep_wait();  // every global access below comes after the previous grid
+    __shared__ int s_run[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const int run = (nblk + 31) / 32, lo = warp * run, hi = min(nblk, lo + run);
+    int sum = 0;
+    if (e < E) {
+#pragma unroll 8
+        for (int b = lo; b < hi; ++b) sum += blk_counts[static_cast<int64_t>(b) * E + e];
+    }
+    s_run[warp][lane] = sum;
+    __syncthreads();
+    int at = 0;
+    for (int w = 0; w < warp; ++w) at += s_run[w][lane];
+    if (e < E) {
+#pragma unroll 8
+        for (int b = lo; b < hi; ++b) {
+            const int c = blk_counts[static_cast<int64_t>(b) * E + e];
+            blk_base[static_cast<int64_t>(b) * E + e] = at;
+            at += c;
+        }
+        if (warp == 31) counts[e] = at;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads)
+topk_scatter_kernel(const int32_t* __restrict__ expert_idx, int64_t pairs, int ppb, int E,
+                    const int32_t* __restrict__ blk_base, const int32_t* __restrict__ counts,
+                    int32_t* __restrict__ offsets, int32_t* __restrict__ perm) {
+    griddep_wait();  // every global access below comes after the previous grid
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_warp[32];
+    __shared__ int s_base[kMaxE];
+    const int e = threadIdx.x;
+    const int off = exclusive_scan_256(e < E ? counts[e] : 0, s_warp);
+    if (e < E) {
+        s_base[e] = off + blk_base[static_cast<int64_t>(blockIdx.x) * E + e];
+        if (blockIdx.x == 0) offsets[e] = off;
+    }
+    if (blockIdx.x == 0 && e == 0) offsets[E] = static_cast<int32_t>(pairs);
+    __syncthreads();
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * ppb;
+    const int n = static_cast<int>(pairs - p0 < ppb ? pairs - p0 : ppb);
+    scatter_pairs<kWarps>(expert_idx + p0, n, static_cast<int32_t>(p0), E, s_base, reinterpret_cast<int*>(smem), perm);
+}
+
+// Gradient of the logits: a token per LPT lanes, its row of gradients built in shared
+// memory (zeros and the K chosen entries) and written as a whole.
+//   renormalised: d l_k = w_k (g_k - sum_j w_j g_j) for the chosen, w summing to 1, times
+//   (1 - s_k) for the sigmoid; softmax: d l_e = s_e (g_e - sum_j s_j g_j), g = 0 for the
+//   others; sigmoid: g_k s_k (1 - s_k).  g: the weight's gradient times scale.
+template <typename T, int LPT, int VPL>
+__global__ void __launch_bounds__(kThreads)
+topk_route_bwd_kernel(const T* __restrict__ logits, int64_t ld, int64_t T_, bool vec_in, bool vec_out, Rule R,
+                      const int32_t* __restrict__ expert_idx, const float* __restrict__ d_weights, T* d_logits,
+                      int accumulate) {
+    griddep_wait();  // every global access below comes after the previous grid
+    __shared__ __align__(16) float s_row[kWarps][32 * VPL];
+    constexpr int TPW = 32 / LPT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LPT, tok = lane / LPT, e0 = sub * VPL;
+    float* row_d = s_row[warp] + tok * LPT * VPL;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * TPW;
+    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * TPW; base < T_; base += step) {
+        const int64_t t = base + tok;
+        const bool valid = t < T_;
+        const T* row = logits + (valid ? t : 0) * ld;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) row_d[e0 + j] = 0.0f;
+        __syncwarp();
+        auto pair = [&](int k, int& e, float& g) {  // an index outside the row is left out
+            e = valid ? expert_idx[t * R.K + k] : -1;
+            if (static_cast<unsigned>(e) >= static_cast<unsigned>(R.E)) e = -1;
+            g = valid ? R.scale * d_weights[t * R.K + k] : 0.0f;
+        };
+        int e;
+        float g;
+        if (R.renorm) {
+            float m = -INFINITY, z = 0.0f, dot = 0.0f;
+            auto unnormalised = [&](float x) {
+                const float p = expf((R.sigmoid && x >= 0.0f ? 0.0f : x) - m);
+                return R.sigmoid ? p / (1.0f + expf(-fabsf(x))) : p;
+            };
+            for (int k = sub; k < R.K; k += LPT) {
+                pair(k, e, g);
+                if (e >= 0) {
+                    const float x = to_f(row[e]);
+                    m = fmaxf(m, R.sigmoid ? fminf(x, 0.0f) : x);
+                }
+            }
+            m = lanes_max<LPT>(m);
+            if (m == -INFINITY) m = 0.0f;
+            for (int k = sub; k < R.K; k += LPT) {
+                pair(k, e, g);
+                if (e >= 0) {
+                    const float p = unnormalised(to_f(row[e]));
+                    z += p;
+                    dot += p * g;
+                }
+            }
+            z = lanes_sum<LPT>(z);
+            dot = lanes_sum<LPT>(dot);
+            const float inv = 1.0f / (z == 0.0f ? 1.0f : z);
+            for (int k = sub; k < R.K; k += LPT) {
+                pair(k, e, g);
+                if (e >= 0) {
+                    const float x = to_f(row[e]);
+                    float d = unnormalised(x) * inv * (g - dot * inv);
+                    if (R.sigmoid) d /= 1.0f + expf(x);
+                    row_d[e] = d;
+                }
+            }
+        } else if (R.sigmoid) {
+            for (int k = sub; k < R.K; k += LPT) {
+                pair(k, e, g);
+                if (e >= 0) {
+                    const float x = to_f(row[e]), q = expf(-fabsf(x));
+                    row_d[e] = g * (q / ((1.0f + q) * (1.0f + q)));  // s (1 - s), the same for x and -x
+                }
+            }
+        } else {
+            for (int k = sub; k < R.K; k += LPT) {
+                pair(k, e, g);
+                if (e >= 0) row_d[e] = g;
+            }
+            __syncwarp();
+            float l[VPL], m, z;
+            load_logits<T, VPL>(row, e0, R.E, vec_in, valid, l);
+            softmax_stats<float, LPT, VPL>(l, e0, R.E, m, z);
+            const float inv = 1.0f / z;
+            float dot = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                l[j] = e0 + j < R.E ? expf(l[j] - m) * inv : 0.0f;
+                dot += l[j] * row_d[e0 + j];
+            }
+            dot = lanes_sum<LPT>(dot);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) row_d[e0 + j] = l[j] * (row_d[e0 + j] - dot);
+        }
+        __syncwarp();
+        if (valid) {
+            T* out = d_logits + t * R.E;
+            constexpr int C = 16 / sizeof(T);
+            if (vec_out) {
+#pragma unroll
+                for (int j = 0; j < VPL; j += C) {
+                    if (e0 + j >= R.E) continue;
+                    Chunk<T, C> o;
+                    if (accumulate) o = *reinterpret_cast<const Chunk<T, C>*>(out + e0 + j);
+#pragma unroll
+                    for (int i = 0; i < C; ++i)
+                        o.v[i] = from_f<T>((accumulate ? to_f(o.v[i]) : 0.0f) + row_d[e0 + j + i]);
+                    *reinterpret_cast<Chunk<T, C>*>(out + e0 + j) = o;
+                }
+            } else {
+                for (int i = sub; i < R.E; i += LPT)
+                    out[i] = from_f<T>((accumulate ? to_f(out[i]) : 0.0f) + row_d[i]);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------- launches
+struct RouteArgs {
+    const void* logits;
+    int64_t ld, T;
+    bool vec;
+    const float* bias;
+    Rule R;
+    moe_routing_t out;
+    float* weights;
+    int32_t* blk_counts;
+    int32_t* blk_base;
+};
+
+// Tokens one block of 32 warps handles in at most two steps take the one-block kernel, if
+// its shared memory holds them. Returns the bytes, 0 if not.
+int small_smem(const RouteArgs& a, int ep, int warp_area) {
+    constexpr int kLimit = 200 * 1024;
+    if (a.T * ep > 2 * 32 * 512 || a.T * a.R.K > kSmallPairs) return 0;
+    const int per_warp = warp_area > a.R.E * 4 ? warp_area : a.R.E * 4;
+    const int smem = kMaxE * 4 + (static_cast<int>(a.T) * a.R.K + 3) / 4 * 16 + kSmallThreads / 32 * per_warp;
+    return smem <= kLimit ? smem : 0;
+}
+
+template <typename T, int LPT, int VPL, bool SCORES>
+cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
+    const Rule& R = a.R;
+    const int wb = warp_bytes(R, LPT, VPL);
+    if (const int smem = small_smem(a, LPT * VPL, wb)) {
+        auto kernel = topk_route_small_kernel<T, LPT, VPL, SCORES>;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(1), dim3(kSmallThreads), smem, s, static_cast<const T*>(a.logits), a.ld,
+                          static_cast<int>(a.T), a.vec, a.bias, R, a.out.expert_idx, a.weights, a.out.counts,
+                          a.out.offsets, a.out.perm);
+    }
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return e;
+    // tokens per block: whole steps of the block's warps, four blocks an SM where there are enough
+    constexpr int step = kWarps * (32 / LPT);
+    const int64_t steps = (a.T + step - 1) / step;
+    int64_t want = static_cast<int64_t>(sms) * 4;
+    if (want > kMaxBlocks) want = kMaxBlocks;
+    const int64_t per = (steps + want - 1) / want;
+    const int tpb = static_cast<int>(per) * step;
+    const int nblk = static_cast<int>((a.T + tpb - 1) / tpb);
+    const int smem = kMaxE * 4 + kWarps * wb;
+    auto kernel = topk_route_kernel<T, LPT, VPL, SCORES>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kernel, dim3(nblk), dim3(kThreads), smem, s, static_cast<const T*>(a.logits), a.ld, a.T, tpb, a.vec,
+                   a.bias, R, a.out.expert_idx, a.weights, a.blk_counts);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(topk_scan_kernel, dim3((R.E + 31) / 32), dim3(1024), 0, s, a.blk_counts, nblk, R.E, a.blk_base,
+                   a.out.counts);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(topk_scatter_kernel, dim3(nblk), dim3(kThreads), kWarps * R.E * 4, s, a.out.expert_idx,
+                      a.T * R.K, tpb * R.K, R.E, a.blk_base, a.out.counts, a.out.offsets, a.out.perm);
+}
+
+template <typename T, bool SCORES>
+cudaError_t route_width(const RouteArgs& a, cudaStream_t s) {
+    const int E = a.R.E;
+    if (E <= 8) return route_launch<T, 1, 8, SCORES>(a, s);
+    if (E <= 16) return route_launch<T, 1, 16, SCORES>(a, s);
+    if (E <= 32) return route_launch<T, 2, 16, SCORES>(a, s);
+    if (E <= 64) return route_launch<T, 4, 16, SCORES>(a, s);
+    if (E <= 128) return route_launch<T, 8, 16, SCORES>(a, s);
+    return route_launch<T, 16, 16, SCORES>(a, s);
+}
+
+template <typename T>
+cudaError_t route_type(const RouteArgs& a, cudaStream_t s) {
+    const bool scores = a.bias || (a.R.G > 1 && a.R.best == 2);
+    return scores ? route_width<T, true>(a, s) : route_width<T, false>(a, s);
+}
+
+template <typename T>
+cudaError_t route_bwd_type(const void* logits, int64_t ld, int64_t T_, bool vec_in, bool vec_out, const Rule& R,
+                           const int32_t* idx, const float* dw, void* out, int acc, cudaStream_t s) {
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return e;
+    auto go = [&](auto kernel, int lpt) {
+        const int64_t tokens = kWarps * (32 / lpt), want = (T_ + tokens - 1) / tokens, cap = static_cast<int64_t>(sms) * 8;
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(kThreads), 0, s,
+                          static_cast<const T*>(logits), ld, T_, vec_in, vec_out, R, idx, dw, static_cast<T*>(out), acc);
+    };
+    if (R.E <= 8) return go(topk_route_bwd_kernel<T, 1, 8>, 1);
+    if (R.E <= 16) return go(topk_route_bwd_kernel<T, 1, 16>, 1);
+    if (R.E <= 32) return go(topk_route_bwd_kernel<T, 2, 16>, 2);
+    if (R.E <= 64) return go(topk_route_bwd_kernel<T, 4, 16>, 4);
+    if (R.E <= 128) return go(topk_route_bwd_kernel<T, 8, 16>, 8);
+    return go(topk_route_bwd_kernel<T, 16, 16>, 16);
+}
+
+moe_status_t check_rule(const moe_topk_rule_t* r, Rule* out) {
+    if (!r) return MOE_ERR_INVALID_ARG;
+    if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (r->flags & ~MOE_TOPK_RENORM) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(r->scale)) return MOE_ERR_INVALID_ARG;
+    if (r->E < 1 || r->E > kMaxE || r->K < 1 || r->K > kMaxK || r->K > r->E) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (r->groups < 1 || r->groups > kMaxGroups || r->E % r->groups != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const int S = r->E / r->groups;
+    if (r->top_groups < 1 || r->top_groups > r->groups || r->top_groups * S < r->K) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (r->group_best < 1 || r->group_best > 2 || r->group_best > S) return MOE_ERR_UNSUPPORTED_SHAPE;
+    *out = Rule{r->E, r->K, r->groups, S, r->top_groups, r->group_best, r->score == MOE_SCORE_SIGMOID ? 1 : 0,
+                (r->flags & MOE_TOPK_RENORM) ? 1 : 0, r->scale};
+    if (r->top_groups == r->groups) out->G = 1, out->S = r->E, out->top_groups = 1;  // every group stays
+    return MOE_OK;
+}
+
+moe_status_t check_tokens(int64_t T, int64_t ld, int E, int K, moe_dtype_t dtype) {
+    if (T < 0 || ld < E || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (T >= kMaxT / K || ld > (int64_t{1} << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+bool rows_vec(const void* p, int E, int64_t ld, size_t b) {
+    const int c = static_cast<int>(16 / b);
+    return E % c == 0 && ld % c == 0 && aligned(p, 16);
+}
+
+size_t strided_bytes(int64_t T, int64_t n, int64_t ld, size_t b) {
+    return T > 0 ? (static_cast<size_t>(T - 1) * ld + n) * b : 0;
+}
+
+}  // namespace
+
+size_t topk_route_ws_bytes(int64_t T, int E) {
+    const int64_t blocks = T < kMaxBlocks ? T : kMaxBlocks;
+    return 256 + 2 * align_up(static_cast<size_t>(blocks) * E * sizeof(int32_t), 256);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_topk_route(const void* logits, moe_dtype_t dtype, int64_t T, int64_t ld, const moe_topk_rule_t* rule,
+                            const float* bias, const moe_routing_t* out, float* weights, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    RouteArgs a{};
+    moe_status_t st = check_rule(rule, &a.R);
+    if (st == MOE_OK) st = check_tokens(T, ld, a.R.E, a.R.K, dtype);
+    if (st != MOE_OK) return st;
+    const int E = a.R.E, K = a.R.K;
+    if (!out || !out->counts || !out->offsets) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!logits || !weights || !out->expert_idx || !out->perm)) return MOE_ERR_INVALID_ARG;
+    const size_t b = dtype_bytes(dtype);
+    if (!aligned(logits, b) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(out->expert_idx, 4) ||
+        !aligned(out->counts, 4) || !aligned(out->offsets, 4) || !aligned(out->perm, 4))
+        return MOE_ERR_MISALIGNED;
+    const size_t pairs = static_cast<size_t>(T) * K;
+    const Range outs[6] = {{out->expert_idx, 4 * pairs}, {out->counts, sizeof(int32_t) * E},
+                           {out->offsets, sizeof(int32_t) * (E + 1)}, {out->perm, 4 * pairs},
+                           {weights, 4 * pairs},       {workspace, workspace ? workspace_bytes : 0}};
+    const Range ins[2] = {{logits, strided_bytes(T, E, ld, b)}, {bias, sizeof(float) * E}};
+    if (any_alias(outs, 6, ins, 2)) return MOE_ERR_ALIAS;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        cudaError_t e = cudaMemsetAsync(out->counts, 0, sizeof(int32_t) * E, s);
+        if (e == cudaSuccess) e = cudaMemsetAsync(out->offsets, 0, sizeof(int32_t) * (E + 1), s);
+        return cuda_status(e);
+    }
+    if (!workspace) return MOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
+    const size_t need = topk_route_ws_bytes(T, E);
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    a.logits = logits;
+    a.ld = ld;
+    a.T = T;
+    a.vec = rows_vec(logits, E, ld, b);
+    a.bias = bias;
+    a.out = *out;
+    a.weights = weights;
+    a.blk_counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
+    a.blk_base = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256 + (need - 256) / 2);
+    if (dtype == MOE_DTYPE_F32) return cuda_status(route_type<float>(a, s));
+    if (dtype == MOE_DTYPE_BF16) return cuda_status(route_type<__nv_bfloat16>(a, s));
+    return cuda_status(route_type<__half>(a, s));
+}
+
+moe_status_t moe_topk_route_bwd(const void* logits, moe_dtype_t dtype, int64_t T, int64_t ld,
+                                const moe_topk_rule_t* rule, const int32_t* expert_idx, const float* d_weights,
+                                void* d_logits, int32_t accumulate, void* stream) {
+    Rule R;
+    moe_status_t st = check_rule(rule, &R);
+    if (st == MOE_OK) st = check_tokens(T, ld, R.E, R.K, dtype);
+    if (st != MOE_OK) return st;
+    if (T > 0 && (!logits || !expert_idx || !d_weights || !d_logits)) return MOE_ERR_INVALID_ARG;
+    const size_t b = dtype_bytes(dtype), pairs = static_cast<size_t>(T) * R.K;
+    if (!aligned(logits, b) || !aligned(d_logits, b) || !aligned(expert_idx, 4) || !aligned(d_weights, 4))
+        return MOE_ERR_MISALIGNED;
+    const Range outs[1] = {{d_logits, static_cast<size_t>(T) * R.E * b}};
+    const Range ins[3] = {{logits, strided_bytes(T, R.E, ld, b)}, {expert_idx, 4 * pairs}, {d_weights, 4 * pairs}};
+    if (any_alias(outs, 1, ins, 3)) return MOE_ERR_ALIAS;
+    if (T == 0) return MOE_OK;
+    const bool vi = rows_vec(logits, R.E, ld, b), vo = rows_vec(d_logits, R.E, R.E, b);
+    const int acc = accumulate ? 1 : 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == MOE_DTYPE_F32)
+        return cuda_status(route_bwd_type<float>(logits, ld, T, vi, vo, R, expert_idx, d_weights, d_logits, acc, s));
+    if (dtype == MOE_DTYPE_BF16)
+        return cuda_status(route_bwd_type<__nv_bfloat16>(logits, ld, T, vi, vo, R, expert_idx, d_weights, d_logits, acc, s));
+    return cuda_status(route_bwd_type<__half>(logits, ld, T, vi, vo, R, expert_idx, d_weights, d_logits, acc, s));
+}
+
+}  // extern "C"

@@ -40,7 +40,10 @@ MOE_NOALLOC_MAX_TOKENS = 2097152
 # The top-k block (include/moe_topk.h).
 MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
 _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
-EXPORTED_TOPK = ["moe_topk_abi_version", "moe_layer_norm_fwd", "moe_layer_norm_workspace_bytes", "moe_layer_norm_bwd"]
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_TOPK_RENORM = 0x1
+EXPORTED_TOPK = ["moe_topk_abi_version", "moe_topk_workspace_bytes", "moe_topk_route", "moe_topk_route_bwd",
+                 "moe_layer_norm_fwd", "moe_layer_norm_workspace_bytes", "moe_layer_norm_bwd"]
 
 
 class MoeError(RuntimeError):
@@ -54,6 +57,12 @@ class MoeError(RuntimeError):
 class RoutingC(ctypes.Structure):
     _fields_ = [("expert_idx", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("perm", ctypes.c_void_p)]
+
+
+class TopKRuleC(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("K", ctypes.c_int32), ("score", ctypes.c_int), ("flags", ctypes.c_uint32),
+                ("scale", ctypes.c_float), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32)]
 
 
 _lib = None
@@ -110,6 +119,13 @@ def lib() -> ctypes.CDLL:
         L.moe_topk_abi_version.restype = I32
         L.moe_topk_abi_version.argtypes = []
         F = ctypes.c_float
+        L.moe_topk_workspace_bytes.restype = SZ
+        L.moe_topk_workspace_bytes.argtypes = [I64, I32, I32, I32]
+        L.moe_topk_route.restype = I32
+        L.moe_topk_route.argtypes = [P, I32, I64, I64, ctypes.POINTER(TopKRuleC), P, ctypes.POINTER(RoutingC), P, P,
+                                     SZ, P]
+        L.moe_topk_route_bwd.restype = I32
+        L.moe_topk_route_bwd.argtypes = [P, I32, I64, I64, ctypes.POINTER(TopKRuleC), P, P, P, I32, P]
         L.moe_layer_norm_fwd.restype = I32
         L.moe_layer_norm_fwd.argtypes = [P, I32, I64, I32, I64, P, P, I32, F, P, P, P, P]
         L.moe_layer_norm_workspace_bytes.restype = SZ
@@ -339,6 +355,69 @@ def _workspace(ws: torch.Tensor | None, dev: int):
     if ws is None:
         return None, 0
     return _arg("ws", ws, dev, torch.uint8, ws.numel()), ws.numel()
+
+
+@dataclasses.dataclass(frozen=True)
+class TopKRule:
+    """How a token's experts are chosen (moe_topk_rule_t)."""
+    E: int
+    K: int
+    score: int = MOE_SCORE_SOFTMAX
+    renorm: bool = False
+    scale: float = 1.0
+    groups: int = 1
+    top_groups: int = 1
+    group_best: int = 1
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", TopKRuleC(self.E, self.K, self.score, MOE_TOPK_RENORM if self.renorm else 0,
+                                                 self.scale, self.groups, self.top_groups, self.group_best))
+
+
+def moe_topk_workspace_bytes(T: int, E: int, K: int, H: int = 0) -> int:
+    return int(lib().moe_topk_workspace_bytes(T, E, K, H))
+
+
+def new_topk_workspace(T: int, E: int, K: int, H: int, device, stream=None) -> torch.Tensor:
+    """Allocates (torch) and initialises a workspace for the top-k calls on T tokens, E
+    experts, K experts per token and H channels (H = 0: the router only)."""
+    ws = torch.empty(max(moe_topk_workspace_bytes(T, E, K, H), 256), dtype=torch.uint8, device=device)
+    moe_top1_workspace_init(ws, stream)
+    return ws
+
+
+def _pairs(routing: Routing, dev: int, pairs: int, E: int) -> RoutingC:
+    i = torch.int32
+    return RoutingC(_arg("expert_idx", routing.expert_idx, dev, i, pairs), _arg("counts", routing.counts, dev, i, E),
+                    _arg("offsets", routing.offsets, dev, i, E + 1), _arg("perm", routing.perm, dev, i, pairs))
+
+
+def moe_topk_route(logits, rule: TopKRule, bias, routing: Routing, weights, ws: torch.Tensor, stream=None):
+    """Chooses rule.K experts for every row of logits [T, E] (rows may be strided) and
+    writes their weights [T, K] and the routing of the T * K pairs. bias [E] or None."""
+    dev, dt, T, E, ld = _rows("logits", logits)
+    if E != rule.E:
+        raise ValueError(f"logits: expected {rule.E} columns, got {E}")
+    rc = _pairs(routing, dev, T * rule.K, E)
+    f = torch.float32
+    w, n = _workspace(ws, dev)
+    _check("moe_topk_route",
+           lib().moe_topk_route(logits.data_ptr(), _DTYPES[dt], T, ld, rule._c, _arg("bias", bias, dev, f, E), rc,
+                                _arg("weights", weights, dev, f, T, rule.K), w, n, _stream(stream)))
+
+
+def moe_topk_route_bwd(logits, rule: TopKRule, expert_idx, d_weights, d_logits, accumulate: bool = False, stream=None):
+    """Gradient of the logits from the weights' gradient d_weights [T, K]; expert_idx is
+    the routing's, [T * K] or [T, K]."""
+    dev, dt, T, E, ld = _rows("logits", logits)
+    if E != rule.E:
+        raise ValueError(f"logits: expected {rule.E} columns, got {E}")
+    _check("moe_topk_route_bwd",
+           lib().moe_topk_route_bwd(logits.data_ptr(), _DTYPES[dt], T, ld, rule._c,
+                                    _arg("expert_idx", expert_idx.view(-1), dev, torch.int32, T * rule.K),
+                                    _arg("d_weights", d_weights, dev, torch.float32, T, rule.K),
+                                    _arg("d_logits", d_logits, dev, dt, T, E), 1 if accumulate else 0,
+                                    _stream(stream)))
 
 
 def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:

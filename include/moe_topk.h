@@ -28,7 +28,7 @@
 extern "C" {
 #endif
 
-/* 1: layer norm, both directions. */
+/* 1: layer norm and the router, both directions. */
 #define MOE_TOPK_ABI_VERSION 1
 
 /* Element types. */
@@ -40,6 +40,76 @@ typedef enum {
 
 /* MOE_TOPK_ABI_VERSION of the built library. */
 int32_t moe_topk_abi_version(void);
+
+/* How logits become scores. */
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0, /* softmax over the E experts */
+    MOE_SCORE_SIGMOID = 1  /* the logistic function of each logit */
+} moe_score_t;
+
+#define MOE_TOPK_RENORM 0x1u /* the K weights of a token are divided by their sum */
+
+/* The rule that chooses experts. */
+typedef struct {
+    int32_t E;          /* experts, 1 .. 256 */
+    int32_t K;          /* experts per token, 1 .. 16, at most E */
+    moe_score_t score;
+    uint32_t flags;     /* MOE_TOPK_RENORM or 0 */
+    float scale;        /* factor of every weight, finite */
+    int32_t groups;     /* 1 .. 32, a divisor of E: groups of E / groups neighbouring experts */
+    int32_t top_groups; /* groups a token may choose from; top_groups * (E / groups) >= K */
+    int32_t group_best; /* 1 or 2, at most E / groups: a group's score is the sum of its best ones */
+} moe_topk_rule_t;
+
+/* Bytes of workspace for T tokens, E experts, K experts per token and H channels:
+ * enough for moe_topk_route, and with H > 0 for the experts' calls too. 0 for sizes
+ * that no call accepts. */
+size_t moe_topk_workspace_bytes(int64_t T, int32_t E, int32_t K, int32_t H);
+
+/*
+ * Router. For every token t, from logits[t, 0..E) (elements of `dtype`, rows ld >= E
+ * elements apart):
+ *   s[e] = softmax or logistic function of the logits,   v[e] = s[e] + bias[e]
+ *   an expert whose logit is -inf or NaN (or whose v is NaN, as every softmax score
+ *     of a row with a NaN or +inf is) is masked: v[e] = -inf, behind all others
+ *   with groups: a group's score is the sum of its group_best largest v; the
+ *     top_groups groups with the largest scores stay (ties: the lower group)
+ *   the K experts with the largest v among those that stay are chosen, largest
+ *     first (ties: the lower index)
+ *   weights[t, k] = scale * s[e_k], or with MOE_TOPK_RENORM
+ *     scale * s[e_k] / sum_j s[e_j]
+ * bias [E] (float, finite; NULL: none) takes part in the choice only. Choices are
+ * those of exact arithmetic on the given logits and bias, as far as fp64 tells two
+ * values apart; without a bias the experts' order is that of the logits themselves.
+ * Renormalised weights are ratios of exponentials and do not depend on the scores
+ * being representable. Where a token has fewer than K unmasked experts to choose
+ * from, masked ones fill up, with the weight of their score (-inf: 0); a row of
+ * nothing but -inf gives experts by index with weights 0.
+ *
+ * out: expert_idx [T * K] (pair p = t * K + k), counts [E] and offsets [E + 1] over
+ * pairs, and perm [T * K], the pairs grouped by expert, ascending inside a group.
+ * weights [T * K] float. T = 0 zeroes counts and offsets. 0 <= T, T * K < 2^31 - 256.
+ * Outputs overlap neither each other nor an input. Needs the workspace.
+ */
+moe_status_t moe_topk_route(const void* logits, moe_dtype_t dtype, int64_t T, int64_t ld,
+                            const moe_topk_rule_t* rule, const float* bias, const moe_routing_t* out,
+                            float* weights, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the logits through the weights, the choice held fixed: with
+ * g[k] = scale * d_weights[t, k] on the chosen experts,
+ *   softmax:               d[e]   = s[e] (g[e] - sum_k s[e_k] g[k]),  g[e] = 0 if e is not chosen
+ *   sigmoid:               d[e_k] = g[k] s (1 - s)
+ *   renormalised softmax:  d[e_k] = r[k] (g[k] - sum_j r[j] g[j]),   r = s / sum of the chosen s
+ *   renormalised sigmoid:  d[e_k] = r[k] (g[k] - sum_j r[j] g[j]) (1 - s[e_k])
+ * and 0 for all other experts. d_logits [T, E] is dense, of the logits' type;
+ * accumulate = 1 adds to it (a balance loss's gradient, say), 0 overwrites it. The
+ * balance bias has no gradient. Experts outside [0, E) in expert_idx are left out.
+ * d_logits overlaps no input. No workspace.
+ */
+moe_status_t moe_topk_route_bwd(const void* logits, moe_dtype_t dtype, int64_t T, int64_t ld,
+                                const moe_topk_rule_t* rule, const int32_t* expert_idx,
+                                const float* d_weights, void* d_logits, int32_t accumulate, void* stream);
 
 /*
  * Layer norm over the last axis of x [T, H]:

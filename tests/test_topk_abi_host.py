@@ -88,6 +88,74 @@ def test_layer_norm_workspace_bytes(L):
     assert f(-1, 64) == 0 and f(5, 0) == 0 and f(5, 8193) == 0 and f(2 ** 31, 64) == 0
 
 
+def rule(**k):
+    v = dict(E=64, K=6, score=1, flags=1, scale=2.5, groups=8, top_groups=4, group_best=2)
+    v.update(k)
+    return ops.TopKRuleC(*(v[n] for n, _ in ops.TopKRuleC._fields_))
+
+
+BAD_RULES = [
+    (dict(score=2), INVALID), (dict(flags=2), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(E=0, K=0), SHAPE), (dict(E=257, groups=1, top_groups=1), SHAPE),
+    (dict(K=0), SHAPE), (dict(K=17), SHAPE), (dict(E=4, K=5, groups=1, top_groups=1), SHAPE), (dict(groups=0), SHAPE),
+    (dict(groups=7), SHAPE), (dict(groups=64, top_groups=8, group_best=1), SHAPE), (dict(top_groups=0), SHAPE),
+    (dict(top_groups=9), SHAPE), (dict(K=9, top_groups=1), SHAPE), (dict(group_best=0), SHAPE),
+    (dict(group_best=3), SHAPE), (dict(E=32, groups=32, top_groups=8, group_best=2), SHAPE),
+]
+
+
+def route(L, r=None, **k):
+    v = dict(x=A[0], dtype=F32, T=10, ld=64, bias=A[1], idx=A[2], counts=A[3], offsets=A[4], perm=A[5], w=A[6], ws=A[7],
+             n=1 << 20)
+    v.update(k)
+    out = ops.RoutingC(v["idx"], v["counts"], v["offsets"], v["perm"])
+    return L.moe_topk_route(v["x"], v["dtype"], v["T"], v["ld"], r or rule(), v["bias"], out, v["w"], v["ws"], v["n"], None)
+
+
+def route_bwd(L, r=None, **k):
+    v = dict(x=A[0], dtype=F32, T=10, ld=64, idx=A[2], dw=A[3], d=A[4])
+    v.update(k)
+    return L.moe_topk_route_bwd(v["x"], v["dtype"], v["T"], v["ld"], r or rule(), v["idx"], v["dw"], v["d"], 0, None)
+
+
+@pytest.mark.parametrize("change,status", BAD_RULES)
+def test_rules_that_no_call_accepts(L, change, status):
+    r = rule(**change)
+    assert route(L, r, ld=300) == status
+    assert route_bwd(L, r, ld=300) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=-1), INVALID), (dict(ld=63), INVALID), (dict(dtype=5), INVALID), (dict(x=None), INVALID),
+    (dict(w=None), INVALID), (dict(idx=None), INVALID), (dict(counts=None), INVALID), (dict(offsets=None), INVALID),
+    (dict(perm=None), INVALID), (dict(T=2 ** 31 // 6), SHAPE), (dict(ld=2 ** 31 + 1), SHAPE),
+    (dict(x=A[0] + 2), MISALIGNED), (dict(bias=A[1] + 2), MISALIGNED), (dict(w=A[6] + 1), MISALIGNED),
+    (dict(perm=A[5] + 2), MISALIGNED), (dict(ws=A[7] + 128), MISALIGNED), (dict(ws=None), WORKSPACE),
+    (dict(n=256), WORKSPACE), (dict(idx=A[0] + 2556), ALIAS), (dict(perm=A[2] + 236), ALIAS), (dict(w=A[1] + 252), ALIAS),
+    (dict(counts=A[4] + 4), ALIAS), (dict(x=A[7]), ALIAS), (dict(bias=A[7] + 4096), ALIAS), (dict(w=A[7] + 512), ALIAS),
+])
+def test_route_refuses(L, change, status):
+    assert route(L, **change) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=-1), INVALID), (dict(ld=1), INVALID), (dict(x=None), INVALID), (dict(idx=None), INVALID),
+    (dict(dw=None), INVALID), (dict(d=None), INVALID), (dict(d=A[4] + 2), MISALIGNED), (dict(dw=A[3] + 2), MISALIGNED),
+    (dict(d=A[0]), ALIAS), (dict(d=A[3] + 16), ALIAS), (dict(T=0), OK), (dict(T=0, x=None, d=None), OK),
+])
+def test_route_bwd_refuses(L, change, status):
+    assert route_bwd(L, **change) == status
+
+
+def test_topk_workspace_bytes(L):
+    f = L.moe_topk_workspace_bytes
+    assert f(1, 64, 6, 0) == 256 + 2 * 256 and f(0, 64, 6, 0) == 256
+    assert f(10 ** 6, 256, 8, 0) == 256 + 2 * 1024 * 1024
+    for bad in ((-1, 8, 2, 0), (1, 0, 1, 0), (1, 257, 1, 0), (1, 8, 0, 0), (1, 8, 9, 0), (1, 64, 17, 0), (2 ** 31, 8, 1, 0),
+                (1, 8, 2, -1)):
+        assert f(*bad) == 0
+
+
 def test_binding_refuses_tensors_it_cannot_pass():
     with pytest.raises(ValueError):
         ops.moe_layer_norm_fwd(torch.zeros(2, 4), None, None, 1e-5, torch.zeros(2, 4))
