@@ -17,5 +17,8 @@ cudaError_t device_sms(int* out);
 
 // Workspace of the router: the reserved head, then per-block counts and bases.
 size_t topk_route_ws_bytes(int64_t T, int E);
+// The same with the experts' areas behind it, for sizes the experts' calls accept.
+size_t topk_experts_ws_bytes(int64_t T, int E, int K, int H);
+bool topk_experts_sizes_ok(int64_t T, int E, int K, int H);
 
 }  // namespace moe

@@ -35,5 +35,6 @@ extern "C" int32_t moe_topk_abi_version(void) { return MOE_TOPK_ABI_VERSION; }
 extern "C" size_t moe_topk_workspace_bytes(int64_t T, int32_t E, int32_t K, int32_t H) {
     using namespace moe;
     if (T < 0 || E < 1 || E > 256 || K < 1 || K > 16 || K > E || T >= kMaxT / K || H < 0) return 0;
-    return topk_route_ws_bytes(T, E);
+    if (H == 0) return topk_route_ws_bytes(T, E);
+    return topk_experts_sizes_ok(T, E, K, H) ? topk_experts_ws_bytes(T, E, K, H) : 0;
 }

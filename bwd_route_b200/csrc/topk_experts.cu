@@ -1,0 +1,1102 @@
+// topk_experts.cu -- the experts' weighted product of the top-k block and its gradients,
+// on tcgen05 (bf16 or fp16 operands, fp32 accumulators in tensor memory).
+//
+//   y_t    = sum_k w_tk (W_e x_t + b_e),  e = e_tk
+//   d_x_t  = sum_k w_tk W_e^T g_t
+//   d_w_tk = g_t . (W_e x_t + b_e) = x_t . (W_e^T g_t) + g_t . b_e
+//   dW_e   = sum over the pairs of e of w g x^T,   db_e = sum of w g
+//
+// The pairs (t, k) of an expert are contiguous in the routing's perm, so every expert is
+// a dense product over rows gathered on the fly.
+//
+//   pair_kernel   : y and d_x. Persistent, one block per SM; a tile is 128 pairs of one
+//     expert x BN outputs. Four warps gather the rows by cp.async into a swizzled ring,
+//     one warp streams the expert's weights by TMA (K-major for y, MN-major for d_x), one
+//     thread issues the MMAs into one of two tensor-memory accumulators, eight warps
+//     drain the other. The K rows of a token come from different tiles. Each tile's part
+//     of a row is rounded to the output's type and kept in the workspace until the last
+//     of the K is there: whoever finishes last (a counter per token and column block)
+//     adds the K rows in the order of k and writes the output, so the sum has one
+//     order and one rounding per row whatever the order of arrival, and no second pass
+//     reads the rows again. The backward also takes x . (W_e^T g) from the fp32
+//     accumulators, before any rounding.
+//   dweights_kernel: d_w from those column parts and g . b_e.
+//   wgrad_kernel  : dW and db. The pairs are the contraction index: both operands are
+//     MN-major. Four warps load rows of g, scale them by w (rounded to the operand type)
+//     and store them to shared memory, four gather rows of x; a unit is a 256 x 256 tile
+//     of dW[e] over a piece of e's pairs (topk_plan.h).
+//   wgrad_sum_kernel: adds the pieces of cut experts in order; zeros for experts without
+//     pairs.
+#include <cmath>
+#include <cstdint>
+
+#include "checks.h"
+#include "common.cuh"
+#include "elem.cuh"
+#include "internal.h"
+#include "moe_topk.h"
+#include "topk.h"
+#include "topk_plan.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxE = 256, kMaxK = 16, kMaxH = 4096;
+constexpr unsigned kFull = 0xffffffffu;
+
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (both operands fp16 or both bf16), fp32 sums.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+template <typename T>
+struct MmaFormat;
+template <>
+struct MmaFormat<__half> {
+    static constexpr uint32_t value = 0;
+};
+template <>
+struct MmaFormat<__nv_bfloat16> {
+    static constexpr uint32_t value = 1;
+};
+
+// Instruction descriptor of kind::f16 with fp32 accumulation; mn: the operand is MN-major.
+template <typename T>
+__device__ __forceinline__ uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
+    return (1u << 4) | (MmaFormat<T>::value << 7) | (MmaFormat<T>::value << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// MN-major 16-bit operand, 128-byte swizzle: rows along K of 64 elements (128 bytes) of M or N; 8-row groups along K
+// are 1024 bytes apart (SBO), groups of 64 elements along M or N lbo_bytes apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t lbo_bytes) { return sw128_desc(addr, lbo_bytes, 1024); }
+
+__device__ __forceinline__ int load_acquire(const int* p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ldcg_u4(const void* p) { return __ldcg(static_cast<const uint4*>(p)); }
+
+template <typename T>
+__device__ __forceinline__ void add8(float (&s)[8], uint4 v) {
+    const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += to_f(e[i]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&s)[8]) {
+    uint4 v;
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = from_f<T>(s[i]);
+    return v;
+}
+
+__device__ __forceinline__ void st_shared_u4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Largest i with start[i] <= v (start ascending, start[0] = 0 <= v < start[n]; empty spans skipped).
+__device__ __forceinline__ int span_of(const int* start, int n, int v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// start[i] = exclusive sum of count(0 .. i), start[n] = total; one warp, n <= 32 * 8.
+template <typename F>
+__device__ __forceinline__ void warp_starts(int* start, int n, F count) {
+    const int lane = threadIdx.x & 31;
+    int carry = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const int c = i < n ? count(i) : 0;
+        int incl = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int u = __shfl_up_sync(kFull, incl, off);
+            if (lane >= off) incl += u;
+        }
+        if (i < n) start[i] = carry + incl - c;
+        carry += __shfl_sync(kFull, incl, 31);
+    }
+    if (lane == 0) start[n] = carry;
+}
+
+// ---------------------------------------------------------------- y and d_x
+// Warps 0-7 epilogue (tensor-memory quadrant w % 4, column half w / 4), 8-11 row gather,
+// 12 MMA issuer and tensor-memory owner, 13 weight loader.
+constexpr int kPairThreads = 448;
+constexpr int kPEpiWarps = 8, kPProducer0 = 256, kPMmaWarp = 12, kPLoadWarp = 13;
+constexpr int kMaxStages = 8;
+
+struct __align__(8) PairCtl {
+    uint64_t afull[kMaxStages], aempty[kMaxStages], bfull[kMaxStages], bempty[kMaxStages];
+    uint64_t tfull[2], tempty[2];
+    uint32_t tmem_base;
+    int abort;
+    int off[kMaxE + 1];
+    int tstart[kMaxE + 1];
+};
+
+template <int BN>
+struct PairCfg {
+    static constexpr int BM = 128;
+    static constexpr int A_BYTES = BM * 128;
+    static constexpr int B_BYTES = BN * 128;
+    static constexpr int A_STAGES = BN == 256 ? 5 : 6;
+    static constexpr int B_STAGES = BN == 256 ? 3 : 5;
+    static constexpr int RING_BYTES = A_STAGES * A_BYTES + B_STAGES * B_BYTES;
+    static constexpr int CS = BN >= 128 ? 64 : 32;         // columns of one epilogue step
+    static constexpr int STG_BYTES = kPEpiWarps * 32 * CS * 2;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int SMEM_BYTES = 1024 + RING_BYTES + STG_BYTES + static_cast<int>(sizeof(PairCtl));
+    static_assert(A_STAGES <= kMaxStages && B_STAGES <= kMaxStages, "stages");
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+struct PairArgs {
+    const void* src;       // rows of tokens: x (y) or d_out (d_x)
+    const void* other;     // d_x: x, for the weights' gradient (may be NULL)
+    const void* bias;      // y: may be NULL
+    const float* weights;  // [P]
+    const int32_t* offsets;
+    const int32_t* perm;
+    int E, K, H;
+    int64_t P;
+    void* out;             // [T][H]; d_x: may be NULL (only the weights' gradient)
+    void* scratch;         // [P][H], K > 1
+    int* count;            // [T][NB], zero, K > 1
+    float* dw_part;        // [NB][P], d_x with `other`
+    uint32_t* flags;
+};
+
+// DX = false: B_e[n][k] = W[e][n][k], K-major. DX = true: B_e[n][k] = W[e][k][n], MN-major
+// straight from W.
+template <typename T, int BN, bool DX>
+__global__ void __launch_bounds__(kPairThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
+    using C = PairCfg<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* aring = smem;
+    uint8_t* bring = smem + C::A_STAGES * C::A_BYTES;
+    uint8_t* stg = smem + C::RING_BYTES;
+    PairCtl* ctl = reinterpret_cast<PairCtl*>(smem + C::RING_BYTES + C::STG_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = A.H, K = A.K;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::A_STAGES; ++s) {
+            mbar_init(&ctl->afull[s], 128);  // 128 gather threads
+            mbar_init(&ctl->aempty[s], 1);   // tcgen05.commit
+        }
+        for (int s = 0; s < C::B_STAGES; ++s) {
+            mbar_init(&ctl->bfull[s], 1);    // arrive.expect_tx + TMA bytes
+            mbar_init(&ctl->bempty[s], 1);   // tcgen05.commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl->tfull[b], 1);
+            mbar_init(&ctl->tempty[b], kPEpiWarps);
+        }
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kPLoadWarp && lane == 0) tma_prefetch_desc(&tm_w);
+    if (warp == kPMmaWarp) {
+        tmem_alloc(&ctl->tmem_base, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    griddep_wait();  // the prologue above overlaps the previous kernel; global memory from here on
+    for (int e = threadIdx.x; e <= A.E; e += kPairThreads) ctl->off[e] = A.offsets[e];
+    __syncthreads();
+    if (warp == 0)
+        warp_starts(ctl->tstart, A.E, [&](int e) { return (ctl->off[e + 1] - ctl->off[e] + C::BM - 1) / C::BM; });
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    const int NT = (H + BN - 1) / BN, KCH = H / 64;
+    const int ntiles = ctl->tstart[A.E] * NT;  // below 2^31: checked by the caller
+    volatile int* abort = &ctl->abort;
+    auto tile_rows = [&](int tile, int& e, int& row0, int& nrows) {
+        const int mt = tile / NT;
+        e = span_of(ctl->tstart, A.E, mt);
+        row0 = ctl->off[e] + (mt - ctl->tstart[e]) * C::BM;
+        nrows = min(C::BM, ctl->off[e + 1] - row0);
+    };
+
+    if (warp >= kPProducer0 / 32 && warp < kPProducer0 / 32 + 4) {
+        // ---------------- row gather: 16 bytes per lane, 8 lanes per 128-byte row segment
+        const T* src = static_cast<const T*>(A.src);
+        const int ptid = threadIdx.x - kPProducer0;
+        const int prow = ptid >> 3, pg = ptid & 7;
+        int tok[8], nxt[8];
+        auto load_tokens = [&](int tile, int (&t)[8]) {
+            int e, row0, nrows;
+            tile_rows(tile, e, row0, nrows);
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const int r = it * 16 + prow;
+                t[it] = r < nrows ? A.perm[row0 + r] / K : -1;
+            }
+        };
+        if (static_cast<int>(blockIdx.x) < ntiles) load_tokens(blockIdx.x, tok);
+        int sa = 0;
+        uint32_t pa = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+            if (tile + static_cast<int>(gridDim.x) < ntiles) load_tokens(tile + gridDim.x, nxt);
+            for (int kc = 0; kc < KCH; ++kc) {
+                if (!(ok = mbar_wait(&ctl->aempty[sa], pa ^ 1, abort, A.flags))) break;
+                const uint32_t a_u32 = smem_u32(aring + sa * C::A_BYTES);
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int r = it * 16 + prow;
+                    const int t = tok[it];
+                    cp_async_16_l2_256(a_u32 + r * 128 + ((pg ^ (r & 7)) << 4),
+                                       src + static_cast<int64_t>(t < 0 ? 0 : t) * H + kc * 64 + pg * 8, t < 0 ? 0u : 16u);
+                }
+                cp_async_arrive_noinc(&ctl->afull[sa]);
+                if (++sa == C::A_STAGES) {
+                    sa = 0;
+                    pa ^= 1;
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < 8; ++it) tok[it] = nxt[it];
+        }
+    } else if (warp == kPLoadWarp) {
+        // ---------------- weight loader. Boxes may reach past the expert's last row or column block
+        // (H not a multiple of BN): those columns of the accumulator are not used.
+        if (lane == 0) {
+            int sb = 0;
+            uint32_t pb = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+                int e, row0, nrows;
+                tile_rows(tile, e, row0, nrows);
+                const int n0 = (tile % NT) * BN;
+                const int ng = DX ? min(BN, H - n0) / 64 : 0;
+                for (int kc = 0; kc < KCH; ++kc) {
+                    if (!(ok = mbar_wait(&ctl->bempty[sb], pb ^ 1, abort, A.flags))) break;
+                    if (DX) {
+                        mbar_arrive_expect_tx(&ctl->bfull[sb], ng * 64 * 128);
+                        for (int g = 0; g < ng; ++g)
+                            tma_load_2d(bring + sb * C::B_BYTES + g * 64 * 128, &tm_w, n0 + g * 64, e * H + kc * 64,
+                                        &ctl->bfull[sb]);
+                    } else {
+                        mbar_arrive_expect_tx(&ctl->bfull[sb], C::B_BYTES);
+                        tma_load_2d(bring + sb * C::B_BYTES, &tm_w, kc * 64, e * H + n0, &ctl->bfull[sb]);
+                    }
+                    if (++sb == C::B_STAGES) {
+                        sb = 0;
+                        pb ^= 1;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kPMmaWarp) {
+        // ---------------- MMA issuer (one thread)
+        if (lane == 0) {
+            int sa = 0, sb = 0;
+            uint32_t pa = 0, pb = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+                if (!(ok = mbar_wait(&ctl->tempty[acc], acc_phase ^ 1, abort, A.flags))) break;
+                tc_fence_after();
+                const uint32_t idesc = idesc_f16<T>(128, min(BN, H - (tile % NT) * BN), 0, DX ? 1 : 0);
+                const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+                for (int kc = 0; kc < KCH; ++kc) {
+                    if (!(ok = mbar_wait(&ctl->afull[sa], pa, abort, A.flags))) break;
+                    if (!(ok = mbar_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
+                    fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(aring + sa * C::A_BYTES);
+                    const uint32_t b_addr = smem_u32(bring + sb * C::B_BYTES);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t bdesc = DX ? mn_desc(b_addr + ks * 2048, 64 * 128) : sw128_desc(b_addr + ks * 32, 16, 1024);
+                        mma_f16(d, sw128_desc(a_addr + ks * 32, 16, 1024), bdesc, idesc, (kc | ks) != 0 ? 1u : 0u);
+                    }
+                    mma_commit(&ctl->aempty[sa]);
+                    mma_commit(&ctl->bempty[sb]);
+                    if (++sa == C::A_STAGES) {
+                        sa = 0;
+                        pa ^= 1;
+                    }
+                    if (++sb == C::B_STAGES) {
+                        sb = 0;
+                        pb ^= 1;
+                    }
+                }
+                if (!ok) break;
+                mma_commit(&ctl->tfull[acc]);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1;
+            }
+        }
+        __syncwarp();
+    } else if (warp < kPEpiWarps) {
+        // ---------------- epilogue: this lane's row is 32 (w % 4) + lane; columns of half w / 4
+        constexpr int HALF = BN / 2, CS = C::CS, G = CS / 8;  // G: 16-byte granules of a step's row
+        const int q = warp & 3, half = warp >> 2;
+        const uint32_t my = smem_u32(stg + warp * 32 * CS * 2);
+        const int myrow = 32 * q + lane;
+        const int NB = 2 * NT;
+        T* out = static_cast<T*>(A.out);
+        const bool join = K > 1 && out;  // rows of a token are added up
+        T* scratch = static_cast<T*>(A.scratch);
+        auto tile_pair = [&](int tile) -> int {
+            int e, row0, nrows;
+            tile_rows(tile, e, row0, nrows);
+            return myrow < nrows ? A.perm[row0 + myrow] : -1;
+        };
+        int p_next = static_cast<int>(blockIdx.x) < ntiles ? tile_pair(blockIdx.x) : -1;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
+            int e, row0, nrows;
+            tile_rows(tile, e, row0, nrows);
+            const int p = p_next;
+            if (tile + static_cast<int>(gridDim.x) < ntiles) p_next = tile_pair(tile + gridDim.x);
+            const float w = p >= 0 ? A.weights[p] : 0.0f;
+            const int t = p >= 0 ? p / K : 0;
+            const int nt = tile % NT, col0 = nt * BN + half * HALF;
+            const int ncols = min(HALF, H - col0);  // <= 0: none of this half (the barriers still are)
+            if (!mbar_wait(&ctl->tfull[acc], acc_phase, abort, A.flags)) break;
+            __syncwarp();
+            tc_fence_after();
+            int* count = A.count + static_cast<int64_t>(t) * NB + nt * 2 + half;
+            // every other row of the token is there: add them to this one and write the output
+            const bool last = join && p >= 0 && ncols > 0 && load_acquire(count) == K - 1;
+            const unsigned last_mask = __ballot_sync(kFull, last);
+            const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * BN + half * HALF);
+            float dot = 0.0f;
+            for (int c = 0; c < ncols; c += CS) {
+#pragma unroll
+                for (int h = 0; h < CS / 32; ++h) {
+                    float v[32];
+                    tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c + 32 * h), v);
+                    const int col = col0 + c + 32 * h;
+                    if (DX) {
+                        if (A.other && p >= 0) {
+                            const T* xr = static_cast<const T*>(A.other) + static_cast<int64_t>(t) * H + col;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const Chunk<T, 8> xv = *reinterpret_cast<const Chunk<T, 8>*>(xr + 8 * g);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) dot += v[8 * g + i] * to_f(xv.v[i]);
+                            }
+                        }
+                    } else if (A.bias) {
+                        const T* br = static_cast<const T*>(A.bias) + static_cast<int64_t>(e) * H + col;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br + 8 * g);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[8 * g + i] += to_f(bv.v[i]);
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float s[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s[i] = v[8 * g + i] * w;  // rounded once to T below
+                        const int gg = 4 * h + g;
+                        st_shared_u4(my + lane * CS * 2 + ((gg ^ (lane & (G - 1))) << 4), pack8<T>(s));
+                    }
+                }
+                if (DX && !out) continue;
+                __syncwarp();
+                constexpr int RPI = 32 / G;  // rows one warp instruction covers
+#pragma unroll
+                for (int it = 0; it < 32 / RPI; ++it) {
+                    const int R = it * RPI + lane / G, j = lane % G;
+                    const uint4 val = ld_shared_u4(my + R * CS * 2 + ((j ^ (R & (G - 1))) << 4));
+                    const int pr = __shfl_sync(kFull, p, R);
+                    if (pr < 0) continue;
+                    const int64_t col = col0 + c + j * 8;
+                    if (K == 1) {
+                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(pr) * H + col) = val;
+                    } else if (!((last_mask >> R) & 1u)) {
+                        *reinterpret_cast<uint4*>(scratch + static_cast<int64_t>(pr) * H + col) = val;
+                    } else {
+                        const int tr = pr / K, kr = pr - tr * K;
+                        float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                        for (int k = 0; k < K; ++k)
+                            add8<T>(s, k == kr ? val : ldcg_u4(scratch + (static_cast<int64_t>(tr) * K + k) * H + col));
+                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(tr) * H + col) = pack8<T>(s);
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tempty[acc]);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+            if (DX && A.other && p >= 0) A.dw_part[static_cast<int64_t>(nt * 2 + half) * A.P + p] = dot;
+            if (join && ncols > 0) {
+                // the rows stored above are visible before they are counted
+                __threadfence();
+                __syncwarp();
+                const bool late = p >= 0 && !last && atomicAdd(count, 1) == K - 1;
+                unsigned todo = __ballot_sync(kFull, late);
+                if (todo) {
+                    __threadfence();
+                    __syncwarp();
+                }
+                while (todo) {  // the other rows came in meanwhile: add all K from memory
+                    const int R = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    const int tr = __shfl_sync(kFull, t, R);
+                    for (int j = lane * 8; j < ncols; j += 32 * 8) {
+                        float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                        for (int k = 0; k < K; ++k)
+                            add8<T>(s, ldcg_u4(scratch + (static_cast<int64_t>(tr) * K + k) * H + col0 + j));
+                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(tr) * H + col0 + j) = pack8<T>(s);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kPMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------- d_w
+// One warp per token: d_w = sum of the column parts of x . (W_e^T g), plus g . b_e.
+template <typename T>
+__global__ void __launch_bounds__(256)
+dweights_kernel(const float* __restrict__ dw_part, int nparts, const T* __restrict__ g, const T* __restrict__ bias,
+                const int32_t* __restrict__ expert_idx, int64_t T_, int K, int H, float* __restrict__ d_weights) {
+    griddep_wait();  // every global access below comes after the previous grid
+    const int lane = threadIdx.x & 31;
+    const int64_t P = T_ * K;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T_; t += static_cast<int64_t>(gridDim.x) * 8) {
+        for (int k = 0; k < K; ++k) {
+            const int64_t p = t * K + k;
+            float s = 0.0f;
+            if (bias) {
+                const T* br = bias + static_cast<int64_t>(expert_idx[p]) * H;
+                for (int c = lane * 8; c < H; c += 256) {
+                    const Chunk<T, 8> gv = *reinterpret_cast<const Chunk<T, 8>*>(g + t * H + c);
+                    const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br + c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s += to_f(gv.v[i]) * to_f(bv.v[i]);
+                }
+            }
+            for (int i = lane; i < nparts; i += 32) s += dw_part[i * P + p];
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+            if (lane == 0) d_weights[p] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dW and db
+// Warps 0-7 epilogue, 8-11 rows of g (scaled), 12-15 rows of x, 16 MMA issuer.
+constexpr int kWThreads = 544;
+constexpr int kWG0 = 256, kWX0 = 384, kWMmaWarp = 16;
+
+struct __align__(8) WCtl {
+    uint64_t full[4], empty[4];
+    uint64_t tfull, tempty;
+    uint32_t tmem_base;
+    int abort;
+    int off[kMaxE + 1];
+    int pstart[kMaxE + 1];  // first piece of each expert
+    int sstart[kMaxE + 1];  // first slot of each expert (experts of two pieces or more)
+    float db[4][32][8];
+};
+
+struct WCfg {
+    static constexpr int KT = 64;                   // pairs per stage
+    static constexpr int GROUP = KT * 128;          // 64 columns of a stage's rows
+    static constexpr int OP = 4 * GROUP;            // 256 columns
+    static constexpr int STAGE = 2 * OP;            // g then x: 64 KiB
+    static constexpr int STAGES = 3;
+    static constexpr int STG = 8 * 32 * 64;         // epilogue staging: 32 rows x 64 bytes a warp
+    static constexpr int SMEM = 1024 + STAGES * STAGE + STG + static_cast<int>(sizeof(WCtl));
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct WgradArgs {
+    const void* x;
+    const void* g;
+    const float* weights;
+    const int32_t* offsets;
+    const int32_t* perm;
+    int E, K, H, extra;
+    int64_t P;
+    void* dW;       // may be NULL (db only)
+    void* db;       // may be NULL
+    float* part;    // [slots][H][H]
+    float* part_db; // [slots][H]
+    uint32_t* flags;
+};
+
+// Pieces and slots of every expert, from the offsets in shared memory (warp 0).
+template <typename CtlT>
+__device__ __forceinline__ void piece_starts(CtlT* ctl, int E, int64_t P, int extra) {
+    warp_starts(ctl->pstart, E, [&](int e) { return wgrad_pieces(ctl->off[e + 1] - ctl->off[e], P, extra); });
+    warp_starts(ctl->sstart, E, [&](int e) {
+        const int n = wgrad_pieces(ctl->off[e + 1] - ctl->off[e], P, extra);
+        return n > 1 ? n : 0;
+    });
+}
+
+struct Unit {
+    int e, piece, pieces, lo, hi, o0, i0;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) {
+    using C = WCfg;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* stg = smem + C::STAGES * C::STAGE;
+    WCtl* ctl = reinterpret_cast<WCtl*>(smem + C::STAGES * C::STAGE + C::STG);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = A.H, K = A.K;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&ctl->full[s], 256);  // 128 threads store g, 128 gather x
+            mbar_init(&ctl->empty[s], 1);   // tcgen05.commit
+        }
+        mbar_init(&ctl->tfull, 1);
+        mbar_init(&ctl->tempty, 8);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWMmaWarp) {
+        tmem_alloc(&ctl->tmem_base, 512);
+        tmem_relinquish();
+    }
+    griddep_wait();  // the prologue above overlaps the previous kernel; global memory from here on
+    for (int e = threadIdx.x; e <= A.E; e += kWThreads) ctl->off[e] = A.offsets[e];
+    __syncthreads();
+    if (warp == 0) piece_starts(ctl, A.E, A.P, A.extra);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    volatile int* abort = &ctl->abort;
+    const int nt = (H + kWTile - 1) / kWTile, tiles = nt * nt;
+    const int nunits = ctl->pstart[A.E] * tiles;
+    auto unit_of = [&](int u) {
+        Unit r;
+        const int piece = u / tiles, tile = u - piece * tiles;
+        r.e = span_of(ctl->pstart, A.E, piece);
+        r.pieces = ctl->pstart[r.e + 1] - ctl->pstart[r.e];
+        r.piece = piece - ctl->pstart[r.e];
+        const int64_t n = ctl->off[r.e + 1] - ctl->off[r.e];
+        r.lo = ctl->off[r.e] + static_cast<int>(n * r.piece / r.pieces);
+        r.hi = ctl->off[r.e] + static_cast<int>(n * (r.piece + 1) / r.pieces);
+        r.o0 = (tile / nt) * kWTile;
+        r.i0 = (tile % nt) * kWTile;
+        return r;
+    };
+
+    if (warp >= kWG0 / 32 && warp < kWG0 / 32 + 4) {
+        // ---------------- rows of g, scaled: a lane has 8 fixed columns, 32 / lanes rows a pass
+        const T* g = static_cast<const T*>(A.g);
+        const int w4 = warp - kWG0 / 32;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
+            const Unit r = unit_of(u);
+            const int cols = min(kWTile, H - r.o0);
+            const bool on = lane * 8 < cols;
+            float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            const uint32_t dst0 = (lane >> 3) * C::GROUP;
+            // this warp's 16 rows of a stage are w4, w4 + 4, ...; lane i < 16 looks row i up
+            auto look = [&](int p0, int& tok, float& wt) {
+                const int i = p0 + w4 + 4 * (lane & 15);
+                const int p = i < r.hi ? A.perm[i] : -1;
+                tok = p >= 0 ? p / K : -1;
+                wt = p >= 0 ? A.weights[p] : 0.0f;
+            };
+            int tok, ntok;
+            float wt, nwt;
+            look(r.lo, tok, wt);
+            for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
+                look(p0 + C::KT, ntok, nwt);
+                if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
+                const uint32_t base = smem_u32(smem + stage * C::STAGE) + dst0;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    Chunk<T, 8> v[8];
+                    float wr[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int tr = __shfl_sync(kFull, tok, b * 8 + i);
+                        wr[i] = __shfl_sync(kFull, wt, b * 8 + i);
+                        if (tr >= 0 && on) v[i] = *reinterpret_cast<const Chunk<T, 8>*>(g + static_cast<int64_t>(tr) * H + r.o0 + lane * 8);
+                        else wr[i] = 0.0f, v[i] = Chunk<T, 8>{};
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = w4 + 4 * (b * 8 + i);
+                        float s[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            s[j] = wr[i] * to_f(v[i].v[j]);
+                            db[j] += s[j];
+                        }
+                        if (on) st_shared_u4(base + row * 128 + (((lane & 7) ^ (row & 7)) << 4), pack8<T>(s));
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&ctl->full[stage]);
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                tok = ntok;
+                wt = nwt;
+            }
+            if (ok && A.db && r.i0 == 0) {
+                // the four warps' sums, in order
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ctl->db[w4][lane][j] = db[j];
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (w4 == 0 && on) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) db[j] = ((ctl->db[0][lane][j] + ctl->db[1][lane][j]) + ctl->db[2][lane][j]) + ctl->db[3][lane][j];
+                    const int o = r.o0 + lane * 8;
+                    if (r.pieces == 1) {
+                        *reinterpret_cast<uint4*>(static_cast<T*>(A.db) + static_cast<int64_t>(r.e) * H + o) = pack8<T>(db);
+                    } else {
+                        float* d = A.part_db + (static_cast<int64_t>(ctl->sstart[r.e]) + r.piece) * H + o;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d[j] = db[j];
+                    }
+                }
+            }
+        }
+    } else if (warp >= kWX0 / 32 && warp < kWX0 / 32 + 4) {
+        // ---------------- rows of x
+        const T* x = static_cast<const T*>(A.x);
+        const int w4 = warp - kWX0 / 32;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
+            const Unit r = unit_of(u);
+            const bool on = lane * 8 < min(kWTile, H - r.i0);
+            const uint32_t dst0 = C::OP + (lane >> 3) * C::GROUP;
+            auto look = [&](int p0) {
+                const int i = p0 + w4 + 4 * (lane & 15);
+                return i < r.hi ? A.perm[i] / K : -1;
+            };
+            int tok = look(r.lo);
+            for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
+                const int ntok = look(p0 + C::KT);
+                if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
+                const uint32_t base = smem_u32(smem + stage * C::STAGE) + dst0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int row = w4 + 4 * i;
+                    const int tr = __shfl_sync(kFull, tok, i);
+                    if (on)
+                        cp_async_16(base + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
+                                    x + static_cast<int64_t>(tr < 0 ? 0 : tr) * H + r.i0 + lane * 8, tr < 0 ? 0u : 16u);
+                }
+                cp_async_arrive_noinc(&ctl->full[stage]);
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                tok = ntok;
+            }
+        }
+    } else if (warp == kWMmaWarp) {
+        // ---------------- MMA issuer: two halves of 128 rows of dW, the tile's columns
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
+                const Unit r = unit_of(u);
+                const int halves = (min(kWTile, H - r.o0) + 127) / 128;
+                const uint32_t idesc = idesc_f16<T>(128, min(kWTile, H - r.i0), 1, 1);
+                if (!(ok = mbar_wait(&ctl->tempty, acc_phase ^ 1, abort, A.flags))) break;
+                tc_fence_after();
+                for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
+                    if (!(ok = mbar_wait(&ctl->full[stage], phase, abort, A.flags))) break;
+                    fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint32_t g_addr = smem_u32(smem + stage * C::STAGE), x_addr = g_addr + C::OP;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        for (int mh = 0; mh < halves; ++mh)
+                            mma_f16(tmem + static_cast<uint32_t>(mh * 256), mn_desc(g_addr + mh * 2 * C::GROUP + ks * 2048, C::GROUP),
+                                    mn_desc(x_addr + ks * 2048, C::GROUP), idesc, (p0 != r.lo || ks != 0) ? 1u : 0u);
+                    mma_commit(&ctl->empty[stage]);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                mma_commit(&ctl->tfull);
+                acc_phase ^= 1;
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ---------------- epilogue: rows 32 (w % 4) + lane of each half, columns of half w / 4
+        const int q = warp & 3, ch = warp >> 2;
+        const uint32_t my = smem_u32(stg + warp * 32 * 64);
+        uint32_t acc_phase = 0;
+        T* dW = static_cast<T*>(A.dW);
+        for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
+            const Unit r = unit_of(u);
+            if (!mbar_wait(&ctl->tfull, acc_phase, abort, A.flags)) break;
+            __syncwarp();
+            tc_fence_after();
+            const int rows = min(kWTile, H - r.o0), cols = min(kWTile, H - r.i0);
+            for (int mh = 0; mh < (rows + 127) / 128 && dW; ++mh) {
+                const int o_first = mh * 128 + 32 * q;
+                if (o_first >= rows) break;  // rows is a multiple of 64, so a warp's 32 are in or out together
+                for (int c = ch * 128; c < min(cols, ch * 128 + 128); c += 32) {
+                    float v[32];
+                    tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(mh * 256 + c), v);
+                    if (r.pieces == 1) {
+                        // 32 rows x 64 bytes through shared memory: 4 lanes a row, 8 rows an instruction
+#pragma unroll
+                        for (int gg = 0; gg < 4; ++gg) {
+                            float s[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) s[i] = v[8 * gg + i];
+                            st_shared_u4(my + lane * 64 + ((gg ^ ((lane >> 1) & 3)) << 4), pack8<T>(s));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int it = 0; it < 4; ++it) {
+                            const int R = it * 8 + (lane >> 2), j = lane & 3;
+                            const uint4 val = ld_shared_u4(my + R * 64 + ((j ^ ((R >> 1) & 3)) << 4));
+                            const int64_t o = r.o0 + o_first + R;
+                            *reinterpret_cast<uint4*>(dW + (static_cast<int64_t>(r.e) * H + o) * H + r.i0 + c + j * 8) = val;
+                        }
+                        __syncwarp();
+                    } else {
+                        // fp32 sums of this piece, two steps of 16 columns
+                        const int64_t slot = static_cast<int64_t>(ctl->sstart[r.e]) + r.piece;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int gg = 0; gg < 4; ++gg)
+                                st_shared_v4(my + lane * 64 + ((gg ^ ((lane >> 1) & 3)) << 4), v[16 * h + 4 * gg],
+                                             v[16 * h + 4 * gg + 1], v[16 * h + 4 * gg + 2], v[16 * h + 4 * gg + 3]);
+                            __syncwarp();
+#pragma unroll
+                            for (int it = 0; it < 4; ++it) {
+                                const int R = it * 8 + (lane >> 2), j = lane & 3;
+                                const float4 val = ld_shared_v4(my + R * 64 + ((j ^ ((R >> 1) & 3)) << 4));
+                                const int64_t o = r.o0 + o_first + R;
+                                *reinterpret_cast<float4*>(A.part + (slot * H + o) * H + r.i0 + c + 16 * h + j * 4) = val;
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tempty);
+            acc_phase ^= 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Expert blockIdx.y: zeros if it has no pairs, the sum of its pieces in order if it was
+// cut; whole pieces were written by wgrad_kernel.
+template <typename T>
+__global__ void __launch_bounds__(256) wgrad_sum_kernel(const WgradArgs A) {
+    griddep_wait();  // every global access below comes after the previous grid
+    __shared__ struct {
+        int off[kMaxE + 1], pstart[kMaxE + 1], sstart[kMaxE + 1];
+    } s;
+    const int e = blockIdx.y, H = A.H;
+    const int n = A.offsets[e + 1] - A.offsets[e];
+    const int pieces = wgrad_pieces(n, A.P, A.extra);
+    if (pieces == 1) return;
+    int64_t slot = 0;
+    if (pieces > 1) {
+        for (int i = threadIdx.x; i <= A.E; i += 256) s.off[i] = A.offsets[i];
+        __syncthreads();
+        if (threadIdx.x < 32) piece_starts(&s, A.E, A.P, A.extra);
+        __syncthreads();
+        slot = s.sstart[e];
+    }
+    const int64_t nW = static_cast<int64_t>(H) * H;
+    auto add = [&](const float* part, int64_t stride, T* out, int64_t count) {
+        for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < count; i += static_cast<int64_t>(gridDim.x) * 1024) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int j = 0; j < pieces; ++j) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(part + (slot + j) * stride + i));
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+            Chunk<T, 4> o;
+            o.v[0] = from_f<T>(a.x);
+            o.v[1] = from_f<T>(a.y);
+            o.v[2] = from_f<T>(a.z);
+            o.v[3] = from_f<T>(a.w);
+            *reinterpret_cast<Chunk<T, 4>*>(out + i) = o;
+        }
+    };
+    if (A.dW) add(A.part, nW, static_cast<T*>(A.dW) + e * nW, nW);
+    if (A.db) add(A.part_db, H, static_cast<T*>(A.db) + static_cast<int64_t>(e) * H, H);
+}
+
+// ---------------------------------------------------------------- launches
+bool weight_map(CUtensorMap* map, const void* W, moe_dtype_t dtype, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+    EncodeTiledFn enc = get_encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+               const_cast<void*>(W), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int BN, bool DX>
+cudaError_t pair_launch(const void* W, moe_dtype_t dtype, const PairArgs& a, int sms, cudaStream_t s) {
+    CUtensorMap map;
+    if (!weight_map(&map, W, dtype, static_cast<uint64_t>(a.E) * a.H, a.H, DX ? 64 : BN)) return cudaErrorInvalidValue;
+    auto kernel = pair_kernel<T, BN, DX>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg<BN>::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    const int64_t hit = a.P < a.E ? a.P : a.E;
+    const int64_t tiles = (a.P / 128 + hit) * ((a.H + BN - 1) / BN);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kPairThreads),
+                      PairCfg<BN>::SMEM_BYTES, s, map, a);
+}
+
+// Columns per tile: 256 where that leaves a tile for every SM, narrower ones for few pairs.
+int tile_columns(int64_t P, int E, int H, int sms) {
+    const int64_t m = P / 128 + (P < E ? P : E);
+    if (H > 128 && m * ((H + 255) / 256) >= sms) return 256;
+    if (H > 64 && m * ((H + 127) / 128) >= sms) return 128;
+    return 64;
+}
+
+template <typename T, bool DX>
+cudaError_t pair_width(const void* W, moe_dtype_t dtype, const PairArgs& a, int sms, cudaStream_t s, int* parts) {
+    const int bn = tile_columns(a.P, a.E, a.H, sms);
+    *parts = 2 * ((a.H + bn - 1) / bn);
+    if (a.K > 1 && a.out) {  // the parts that are there, none yet
+        cudaError_t e = cudaMemsetAsync(a.count, 0, sizeof(int) * (a.P / a.K) * *parts, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (bn == 256) return pair_launch<T, 256, DX>(W, dtype, a, sms, s);
+    if (bn == 128) return pair_launch<T, 128, DX>(W, dtype, a, sms, s);
+    return pair_launch<T, 64, DX>(W, dtype, a, sms, s);
+}
+
+template <typename T>
+cudaError_t wgrad_launch(const WgradArgs& a, int sms, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, WCfg::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t hit = a.P < a.E ? a.P : a.E;
+    const int64_t units = (hit + a.extra) * wgrad_tiles(a.H);
+    e = launch_pdl(wgrad_kernel<T>, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kWThreads), WCfg::SMEM, s, a);
+    if (e != cudaSuccess) return e;
+    int x = (a.H * a.H + 4095) / 4096;
+    if (x > 64) x = 64;
+    return launch_pdl(wgrad_sum_kernel<T>, dim3(x, a.E), dim3(256), 0, s, a);
+}
+
+moe_status_t check_sizes(moe_dtype_t dtype, int64_t T, int E, int K, int H) {
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) return MOE_ERR_INVALID_ARG;
+    if (T < 0) return MOE_ERR_INVALID_ARG;
+    if (E < 1 || E > kMaxE || K < 1 || K > kMaxK || K > E) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (H < 64 || H > kMaxH || H % 64 != 0 || T >= kMaxT / K) return MOE_ERR_UNSUPPORTED_SHAPE;
+    // tile numbers stay in 32 bits
+    if ((T * K / 128 + E + 1) * (H / 64) >= kMaxT) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+template <typename T>
+cudaError_t bwd_type(const void* W, const void* bias, moe_dtype_t dtype, PairArgs a, const WgradArgs& wg, int64_t T_,
+                     const int32_t* expert_idx, float* d_weights, int sms, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (a.out || d_weights) {
+        int parts = 0;
+        e = pair_width<T, true>(W, dtype, a, sms, s, &parts);
+        if (e == cudaSuccess && d_weights) {
+            const int64_t want = (T_ + 7) / 8, cap = static_cast<int64_t>(sms) * 8;
+            e = launch_pdl(dweights_kernel<T>, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s,
+                           static_cast<const float*>(a.dw_part), parts, static_cast<const T*>(a.src),
+                           static_cast<const T*>(bias), expert_idx, T_, a.K, a.H, d_weights);
+        }
+    }
+    if (e == cudaSuccess && (wg.dW || wg.db)) e = wgrad_launch<T>(wg, sms, s);
+    return e;
+}
+
+}  // namespace
+
+size_t topk_experts_ws_bytes(int64_t T, int E, int K, int H) {
+    return experts_ws(T, E, K, H, topk_route_ws_bytes(T, E)).total;
+}
+bool topk_experts_sizes_ok(int64_t T, int E, int K, int H) { return check_sizes(MOE_DTYPE_BF16, T, E, K, H) == MOE_OK; }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dtype_t dtype,
+                          const moe_routing_t* routing, const float* weights, int64_t T, int32_t E, int32_t K,
+                          int32_t H, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+    moe_status_t st = check_sizes(dtype, T, E, K, H);
+    if (st != MOE_OK) return st;
+    if (!routing || !W) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!x || !y || !weights || !routing->offsets || !routing->perm)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(bias, 16) || !aligned(y, 16) || !aligned(weights, 4) ||
+        !aligned(routing->offsets, 4) || !aligned(routing->perm, 4))
+        return MOE_ERR_MISALIGNED;
+    const size_t P = static_cast<size_t>(T) * K, act = 2 * static_cast<size_t>(T) * H;
+    const Range outs[2] = {{y, act}, {workspace, workspace ? workspace_bytes : 0}};
+    const Range ins[6] = {{x, act}, {W, 2 * static_cast<size_t>(E) * H * H}, {bias, 2 * static_cast<size_t>(E) * H},
+                          {weights, 4 * P}, {routing->offsets, sizeof(int32_t) * (E + 1)}, {routing->perm, 4 * P}};
+    if (any_alias(outs, 2, ins, 6)) return MOE_ERR_ALIAS;
+    if (T == 0) return MOE_OK;
+    const ExpertsWs L = experts_ws(T, E, K, H, topk_route_ws_bytes(T, E));
+    if (!workspace) return MOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
+    if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+    int sms = 0, parts = 0;
+    if (device_sms(&sms) != cudaSuccess) return MOE_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    PairArgs a{};
+    a.src = x;
+    a.bias = bias;
+    a.weights = weights;
+    a.offsets = routing->offsets;
+    a.perm = routing->perm;
+    a.E = E;
+    a.K = K;
+    a.H = H;
+    a.P = static_cast<int64_t>(P);
+    a.out = y;
+    a.scratch = ws + L.scratch;
+    a.count = reinterpret_cast<int*>(ws + L.count);
+    a.flags = reinterpret_cast<uint32_t*>(ws);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == MOE_DTYPE_BF16 ? pair_width<__nv_bfloat16, false>(W, dtype, a, sms, s, &parts)
+                                               : pair_width<__half, false>(W, dtype, a, sms, s, &parts));
+}
+
+moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dtype_t dtype, const void* d_out,
+                          const moe_routing_t* routing, const float* weights, int64_t T, int32_t E, int32_t K,
+                          int32_t H, void* d_x, void* dW, void* db, float* d_weights, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    moe_status_t st = check_sizes(dtype, T, E, K, H);
+    if (st != MOE_OK) return st;
+    if (!routing) return MOE_ERR_INVALID_ARG;
+    if (!d_x && !dW && !db && !d_weights) return MOE_OK;
+    if ((d_x || d_weights) && !W) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!d_out || !weights || !routing->offsets || !routing->perm)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (dW || db || d_weights) && !x) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && d_weights && bias && !routing->expert_idx) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(bias, 16) || !aligned(d_out, 16) || !aligned(d_x, 16) ||
+        !aligned(dW, 16) || !aligned(db, 16) || !aligned(d_weights, 4) || !aligned(weights, 4) ||
+        !aligned(routing->offsets, 4) || !aligned(routing->perm, 4) || !aligned(routing->expert_idx, 4))
+        return MOE_ERR_MISALIGNED;
+    const size_t P = static_cast<size_t>(T) * K, act = 2 * static_cast<size_t>(T) * H;
+    const size_t wb = 2 * static_cast<size_t>(E) * H * H, bb = 2 * static_cast<size_t>(E) * H;
+    const Range outs[5] = {{d_x, act}, {dW, wb}, {db, bb}, {d_weights, 4 * P}, {workspace, workspace ? workspace_bytes : 0}};
+    const Range ins[8] = {{x, act}, {W, wb}, {bias, bb}, {d_out, act}, {weights, 4 * P},
+                          {routing->offsets, sizeof(int32_t) * (E + 1)}, {routing->perm, 4 * P},
+                          {routing->expert_idx, 4 * P}};
+    if (any_alias(outs, 5, ins, 8)) return MOE_ERR_ALIAS;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        cudaError_t e = cudaSuccess;
+        if (dW) e = cudaMemsetAsync(dW, 0, wb, s);
+        if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, bb, s);
+        return cuda_status(e);
+    }
+    const ExpertsWs L = experts_ws(T, E, K, H, topk_route_ws_bytes(T, E));
+    if (!workspace) return MOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
+    if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+    int sms = 0;
+    if (device_sms(&sms) != cudaSuccess) return MOE_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    PairArgs a{};
+    a.src = d_out;
+    a.other = d_weights ? x : nullptr;
+    a.weights = weights;
+    a.offsets = routing->offsets;
+    a.perm = routing->perm;
+    a.E = E;
+    a.K = K;
+    a.H = H;
+    a.P = static_cast<int64_t>(P);
+    a.out = d_x;
+    a.scratch = ws + L.scratch;
+    a.count = reinterpret_cast<int*>(ws + L.count);
+    a.dw_part = reinterpret_cast<float*>(ws + L.dw_part);
+    a.flags = reinterpret_cast<uint32_t*>(ws);
+    WgradArgs g{};
+    g.x = x;
+    g.g = d_out;
+    g.weights = weights;
+    g.offsets = routing->offsets;
+    g.perm = routing->perm;
+    g.E = E;
+    g.K = K;
+    g.H = H;
+    g.extra = wgrad_extra(E, H);
+    g.P = static_cast<int64_t>(P);
+    g.dW = dW;
+    g.db = db;
+    g.part = reinterpret_cast<float*>(ws + L.part);
+    g.part_db = reinterpret_cast<float*>(ws + L.part_db);
+    g.flags = a.flags;
+    return cuda_status(dtype == MOE_DTYPE_BF16
+                           ? bwd_type<__nv_bfloat16>(W, bias, dtype, a, g, T, routing->expert_idx, d_weights, sms, s)
+                           : bwd_type<__half>(W, bias, dtype, a, g, T, routing->expert_idx, d_weights, sms, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,70 @@
+// topk_plan.h -- how the experts' kernels of the top-k block cut their work, and the
+// workspace that goes with it.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "moe_topk.h"
+
+namespace moe {
+
+// Weight gradient: dW[e] is cut into kWTile x kWTile tiles, and the pairs of an expert
+// into pieces (see wgrad_pieces); a piece's tile is one unit of work.
+constexpr int kWTile = 256;
+constexpr int kWMinPiece = 128;  // pairs a piece of a cut expert has at least
+constexpr int kWUnits = 148;     // units that fill the GPU
+
+inline int wgrad_tiles(int H) {
+    const int n = (H + kWTile - 1) / kWTile;
+    return n * n;
+}
+// Pieces beyond one per expert that all experts share in proportion to their pairs:
+// enough to fill the GPU once where the experts' tiles alone do not, else two for every
+// three experts, so that an expert with 1.5 times its share is cut and others are not.
+inline int wgrad_extra(int E, int H) {
+    const int tiles = wgrad_tiles(H);
+    if (E * tiles >= kWUnits) return (2 * E + 2) / 3;
+    const int fill = kWUnits / tiles - E;
+    return fill > 0 ? fill : 0;
+}
+// Pieces of an expert with n of the P pairs: at most E + extra in all.
+__host__ __device__ inline int wgrad_pieces(int n, int64_t P, int extra) {
+    if (n <= 0) return 0;
+    int q = 1 + static_cast<int>(static_cast<int64_t>(n) * extra / P);
+    const int most = n / kWMinPiece;
+    if (q > most) q = most < 1 ? 1 : most;
+    return q;
+}
+
+struct ExpertsWs {
+    size_t count = 0;    // int32 [T][2 * ceil(H / 64)]: finished parts of every token's columns
+    size_t scratch = 0;  // elements [T * K][H]: the pairs' rows, K > 1
+    size_t dw_part = 0;  // float [2 * ceil(H / 64)][T * K]
+    size_t part = 0;     // float [2 * extra][H][H]
+    size_t part_db = 0;  // float [2 * extra][H]
+    size_t total = 0;
+};
+
+inline ExpertsWs experts_ws(int64_t T, int E, int K, int H, size_t begin) {
+    ExpertsWs L;
+    const size_t P = static_cast<size_t>(T) * K, nb = 2 * static_cast<size_t>((H + 63) / 64);
+    const size_t slots = 2 * static_cast<size_t>(wgrad_extra(E, H));
+    size_t off = align_up(begin, 256);
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes, 256);
+        return at;
+    };
+    L.count = take(K > 1 ? sizeof(int32_t) * T * nb : 0);
+    L.scratch = take(K > 1 ? 2 * P * H : 0);
+    L.dw_part = take(sizeof(float) * nb * P);
+    L.part = take(sizeof(float) * slots * H * H);
+    L.part_db = take(sizeof(float) * slots * H);
+    L.total = off;
+    return L;
+}
+
+}  // namespace moe

@@ -43,6 +43,7 @@ _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.f
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_TOPK_RENORM = 0x1
 EXPORTED_TOPK = ["moe_topk_abi_version", "moe_topk_workspace_bytes", "moe_topk_route", "moe_topk_route_bwd",
+                 "moe_topk_fwd", "moe_topk_bwd",
                  "moe_layer_norm_fwd", "moe_layer_norm_workspace_bytes", "moe_layer_norm_bwd"]
 
 
@@ -126,6 +127,11 @@ def lib() -> ctypes.CDLL:
                                      SZ, P]
         L.moe_topk_route_bwd.restype = I32
         L.moe_topk_route_bwd.argtypes = [P, I32, I64, I64, ctypes.POINTER(TopKRuleC), P, P, P, I32, P]
+        R = ctypes.POINTER(RoutingC)
+        L.moe_topk_fwd.restype = I32
+        L.moe_topk_fwd.argtypes = [P, P, P, I32, R, P, I64, I32, I32, I32, P, P, SZ, P]
+        L.moe_topk_bwd.restype = I32
+        L.moe_topk_bwd.argtypes = [P, P, P, I32, P, R, P, I64, I32, I32, I32, P, P, P, P, P, SZ, P]
         L.moe_layer_norm_fwd.restype = I32
         L.moe_layer_norm_fwd.argtypes = [P, I32, I64, I32, I64, P, P, I32, F, P, P, P, P]
         L.moe_layer_norm_workspace_bytes.restype = SZ
@@ -418,6 +424,43 @@ def moe_topk_route_bwd(logits, rule: TopKRule, expert_idx, d_weights, d_logits, 
                                     _arg("d_weights", d_weights, dev, torch.float32, T, rule.K),
                                     _arg("d_logits", d_logits, dev, dt, T, E), 1 if accumulate else 0,
                                     _stream(stream)))
+
+
+def _experts(x, W, weights):
+    """(device, dtype, T, E, K, H) of the experts' calls."""
+    dev, dt, T, H, ld = _rows("x", x)
+    if dt == torch.float32:
+        raise TypeError("x: expected bfloat16 or float16, got float32")
+    if ld != H:
+        raise ValueError("x: expected a contiguous tensor")
+    if W.dim() != 3 or weights.dim() != 2:
+        raise ValueError("expected W [E, H, H] and weights [T, K]")
+    return dev, dt, T, W.shape[0], weights.shape[1], H
+
+
+def moe_topk_fwd(x, W, bias, routing: Routing, weights, y, ws: torch.Tensor, stream=None):
+    """y [T, H] = sum_k weights[t, k] (W[e] x[t] + bias[e]) over the K experts of every
+    token (bfloat16 or float16; weights [T, K] float32). bias may be None."""
+    dev, dt, T, E, K, H = _experts(x, W, weights)
+    w, n = _workspace(ws, dev)
+    _check("moe_topk_fwd",
+           lib().moe_topk_fwd(x.data_ptr(), _arg("W", W, dev, dt, E, H, H), _arg("bias", bias, dev, dt, E, H),
+                              _DTYPES[dt], _pairs(routing, dev, T * K, E),
+                              _arg("weights", weights, dev, torch.float32, T, K), T, E, K, H,
+                              _arg("y", y, dev, dt, T, H), w, n, _stream(stream)))
+
+
+def moe_topk_bwd(x, W, bias, d_out, routing: Routing, weights, d_x, dW, db, d_weights, ws: torch.Tensor, stream=None):
+    """Gradients of moe_topk_fwd; d_x, dW, db and d_weights are written where given."""
+    dev, dt, T, E, K, H = _experts(x, W, weights)
+    f = torch.float32
+    w, n = _workspace(ws, dev)
+    _check("moe_topk_bwd",
+           lib().moe_topk_bwd(x.data_ptr(), _arg("W", W, dev, dt, E, H, H), _arg("bias", bias, dev, dt, E, H),
+                              _DTYPES[dt], _arg("d_out", d_out, dev, dt, T, H), _pairs(routing, dev, T * K, E),
+                              _arg("weights", weights, dev, f, T, K), T, E, K, H, _arg("d_x", d_x, dev, dt, T, H),
+                              _arg("dW", dW, dev, dt, E, H, H), _arg("db", db, dev, dt, E, H),
+                              _arg("d_weights", d_weights, dev, f, T, K), w, n, _stream(stream)))
 
 
 def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:

@@ -28,7 +28,7 @@
 extern "C" {
 #endif
 
-/* 1: layer norm and the router, both directions. */
+/* 1: layer norm, the router and the experts' weighted product, both directions. */
 #define MOE_TOPK_ABI_VERSION 1
 
 /* Element types. */
@@ -110,6 +110,41 @@ moe_status_t moe_topk_route(const void* logits, moe_dtype_t dtype, int64_t T, in
 moe_status_t moe_topk_route_bwd(const void* logits, moe_dtype_t dtype, int64_t T, int64_t ld,
                                 const moe_topk_rule_t* rule, const int32_t* expert_idx,
                                 const float* d_weights, void* d_logits, int32_t accumulate, void* stream);
+
+/*
+ * The experts' weighted product. With e = expert_idx[t * K + k] and w = weights[t, k],
+ *   y[t, o] = sum_k w (sum_i W[e, o, i] x[t, i] + bias[e, o])
+ * x, y [T, H], W [E, H, H] (W[e][o][i], y = W x) and bias [E, H] (NULL: none) have
+ * elements of `dtype`, MOE_DTYPE_BF16 or MOE_DTYPE_F16, and are dense and 16-byte
+ * aligned; weights [T * K] float. routing is what moe_topk_route wrote (offsets and
+ * perm are read). Products and sums over i are fp32 on the tensor cores; for K > 1
+ * each of the K rows of a token is rounded to `dtype` before the K are added in fp32
+ * in the order of k, and the sum is rounded once (K = 1: one rounding).
+ * 1 <= E <= 256, 1 <= K <= min(16, E), H a multiple of 64 with 64 <= H <= 4096,
+ * 0 <= T * K < 2^31 - 256. y overlaps no input. Needs the workspace.
+ */
+moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dtype_t dtype,
+                          const moe_routing_t* routing, const float* weights, int64_t T, int32_t E,
+                          int32_t K, int32_t H, void* y, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * Its gradients, from the output's gradient d_out [T, H]:
+ *   d_x[t, i]       = sum_k w sum_o W[e, o, i] d_out[t, o]
+ *   dW[e, o, i]     = sum of w d_out[t, o] x[t, i] over the pairs (t, k) of expert e
+ *   db[e, o]        = sum of w d_out[t, o] over them
+ *   d_weights[t, k] = sum_o d_out[t, o] (sum_i W[e, o, i] x[t, i] + bias[e, o])
+ * d_x, dW and db have elements of `dtype`, d_weights [T * K] is float. Any of them may
+ * be NULL to skip it; an expert without pairs gets zeros in dW and db. d_weights comes
+ * from fp32 sums throughout; d_x rounds as y does above; for dW the rows w d_out are
+ * rounded to `dtype` for the tensor cores (fp32 sums, one rounding at the end), for db
+ * they are not. Sums over tokens have a fixed order. bias is read for d_weights only.
+ * Outputs overlap neither each other nor an input. Needs the workspace.
+ */
+moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dtype_t dtype,
+                          const void* d_out, const moe_routing_t* routing, const float* weights,
+                          int64_t T, int32_t E, int32_t K, int32_t H, void* d_x, void* dW, void* db,
+                          float* d_weights, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Layer norm over the last axis of x [T, H]:

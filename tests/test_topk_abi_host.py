@@ -156,6 +156,62 @@ def test_topk_workspace_bytes(L):
         assert f(*bad) == 0
 
 
+BIG = [0x600000000000 + (i << 32) for i in range(16)]  # 4 GiB apart
+
+
+def experts(L, bwd, **k):
+    v = dict(x=BIG[0], W=BIG[1], b=BIG[2], dtype=BF16, g=BIG[3], idx=BIG[4], counts=BIG[5], offsets=BIG[6], perm=BIG[7],
+             w=BIG[8], T=10, E=8, K=2, H=128, y=BIG[9], dx=BIG[9], dW=BIG[10], db=BIG[11], dw=BIG[12], ws=BIG[13],
+             n=1 << 30)
+    v.update(k)
+    r = None if v.get("no_routing") else ops.RoutingC(v["idx"], v["counts"], v["offsets"], v["perm"])
+    if bwd:
+        return L.moe_topk_bwd(v["x"], v["W"], v["b"], v["dtype"], v["g"], r, v["w"], v["T"], v["E"], v["K"], v["H"], v["dx"],
+                              v["dW"], v["db"], v["dw"], v["ws"], v["n"], None)
+    return L.moe_topk_fwd(v["x"], v["W"], v["b"], v["dtype"], r, v["w"], v["T"], v["E"], v["K"], v["H"], v["y"], v["ws"],
+                          v["n"], None)
+
+
+@pytest.mark.parametrize("bwd", [False, True], ids=["fwd", "bwd"])
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=F32), INVALID), (dict(dtype=9), INVALID), (dict(T=-1), INVALID), (dict(no_routing=True), INVALID),
+    (dict(x=None), INVALID), (dict(W=None), INVALID), (dict(w=None), INVALID), (dict(offsets=None), INVALID),
+    (dict(perm=None), INVALID), (dict(E=0), SHAPE), (dict(E=257), SHAPE), (dict(K=0), SHAPE), (dict(K=9), SHAPE),
+    (dict(E=64, K=17), SHAPE), (dict(H=0), SHAPE), (dict(H=96), SHAPE), (dict(H=4160), SHAPE), (dict(T=2 ** 30), SHAPE),
+    (dict(x=BIG[0] + 8), MISALIGNED), (dict(W=BIG[1] + 2), MISALIGNED), (dict(b=BIG[2] + 8), MISALIGNED),
+    (dict(w=BIG[8] + 2), MISALIGNED), (dict(perm=BIG[7] + 1), MISALIGNED), (dict(ws=BIG[13] + 64), MISALIGNED),
+    (dict(ws=None), WORKSPACE), (dict(n=4096), WORKSPACE), (dict(x=BIG[13]), ALIAS), (dict(perm=BIG[13] + 1024), ALIAS),
+])
+def test_experts_refuse(L, bwd, change, status):
+    assert experts(L, bwd, **change) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(y=None), INVALID), (dict(y=BIG[9] + 8), MISALIGNED), (dict(y=BIG[0]), ALIAS), (dict(y=BIG[2] + 64), ALIAS),
+    (dict(y=BIG[13] + (1 << 20)), ALIAS), (dict(T=0), OK),
+])
+def test_experts_fwd_refuses(L, change, status):
+    assert experts(L, False, **change) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(g=None), INVALID), (dict(idx=None), INVALID), (dict(dx=BIG[9] + 8), MISALIGNED), (dict(dW=BIG[10] + 8), MISALIGNED),
+    (dict(db=BIG[11] + 2), MISALIGNED), (dict(dw=BIG[12] + 2), MISALIGNED), (dict(dx=BIG[3]), ALIAS), (dict(dx=BIG[0]), ALIAS),
+    (dict(db=BIG[10] + 128), ALIAS), (dict(dw=BIG[9] + 64), ALIAS), (dict(dW=BIG[13]), ALIAS),
+    (dict(dx=None, dW=None, db=None, dw=None), OK),
+])
+def test_experts_bwd_refuses(L, change, status):
+    assert experts(L, True, **change) == status
+
+
+def test_experts_workspace_bytes(L):
+    f = L.moe_topk_workspace_bytes
+    assert f(10, 8, 2, 128) > f(10, 8, 2, 0) > 0
+    assert f(1000, 8, 2, 256) >= 2 * 1000 * 2 * 256  # a row of every pair
+    assert f(1000, 8, 1, 256) < f(1000, 8, 2, 256)
+    assert f(10, 8, 2, 96) == 0 and f(10, 8, 2, 8192) == 0
+
+
 def test_binding_refuses_tensors_it_cannot_pass():
     with pytest.raises(ValueError):
         ops.moe_layer_norm_fwd(torch.zeros(2, 4), None, None, 1e-5, torch.zeros(2, 4))
