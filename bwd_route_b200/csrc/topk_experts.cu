@@ -9,22 +9,21 @@
 // The pairs (t, k) of an expert are contiguous in the routing's perm, so every expert is
 // a dense product over rows gathered on the fly.
 //
-//   pair_kernel   : y and d_x. Persistent, one block per SM; a tile is 128 pairs of one
-//     expert x BN outputs. Four warps gather the rows by cp.async into a swizzled ring,
-//     one warp streams the expert's weights by TMA (K-major for y, MN-major for d_x), one
-//     thread issues the MMAs into one of two tensor-memory accumulators, eight warps
-//     drain the other. The K rows of a token come from different tiles. Each tile's part
-//     of a row is rounded to the output's type and kept in the workspace until the last
-//     of the K is there: whoever finishes last (a counter per token and column block)
-//     adds the K rows in the order of k and writes the output, so the sum has one
-//     order and one rounding per row whatever the order of arrival, and no second pass
-//     reads the rows again. The backward also takes x . (W_e^T g) from the fp32
-//     accumulators, before any rounding.
-//   dweights_kernel: d_w from those column parts and g . b_e.
+//   pair_kernel   : rows of y and d_x. Persistent, one block per SM; a tile is 128 pairs
+//     of one expert x BN outputs. Four warps gather the rows by cp.async into a swizzled
+//     ring, one warp streams the expert's weights by TMA (K-major for y, MN-major for
+//     d_x), one thread issues the MMAs into one of two tensor-memory accumulators, eight
+//     warps drain the other. With K = 1 a pair's row is the result; else it goes to the
+//     workspace as fp16 with a power of two per 32 columns (their largest value lands in
+//     [2^14, 2^15)): half of fp32's traffic at 11 bits, finer than bf16's 8, whatever the
+//     magnitude. The backward's epilogue also takes x . (W_e^T g) from the fp32
+//     accumulators, with its warps' rows of x brought in by cp.async beside them.
+//   join_kernel   : adds the K rows of a token in the order of k in fp32, one rounding;
+//     in the backward also d_w from the column parts and g . b_e.
 //   wgrad_kernel  : dW and db. The pairs are the contraction index: both operands are
-//     MN-major. Four warps load rows of g, scale them by w (rounded to the operand type)
-//     and store them to shared memory, four gather rows of x; a unit is a 256 x 256 tile
-//     of dW[e] over a piece of e's pairs (topk_plan.h).
+//     MN-major. Four warps gather rows of g and x by cp.async, eight scale the staged rows
+//     of g by w in place (rounded to the operand type) and add them up for db; a unit is a
+//     256 x 256 tile of dW[e] over a piece of e's pairs (topk_plan.h).
 //   wgrad_sum_kernel: adds the pieces of cut experts in order; zeros for experts without
 //     pairs.
 #include <cmath>
@@ -78,19 +77,6 @@ __device__ __forceinline__ uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) 
 // are 1024 bytes apart (SBO), groups of 64 elements along M or N lbo_bytes apart.
 __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t lbo_bytes) { return sw128_desc(addr, lbo_bytes, 1024); }
 
-__device__ __forceinline__ int load_acquire(const int* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint4 ldcg_u4(const void* p) { return __ldcg(static_cast<const uint4*>(p)); }
-
-template <typename T>
-__device__ __forceinline__ void add8(float (&s)[8], uint4 v) {
-    const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] += to_f(e[i]);
-}
 template <typename T>
 __device__ __forceinline__ uint4 pack8(const float (&s)[8]) {
     uint4 v;
@@ -151,7 +137,7 @@ struct __align__(8) PairCtl {
     int tstart[kMaxE + 1];
 };
 
-template <int BN>
+template <int BN, bool DX>
 struct PairCfg {
     static constexpr int BM = 128;
     static constexpr int A_BYTES = BM * 128;
@@ -159,8 +145,10 @@ struct PairCfg {
     static constexpr int A_STAGES = BN == 256 ? 5 : 6;
     static constexpr int B_STAGES = BN == 256 ? 3 : 5;
     static constexpr int RING_BYTES = A_STAGES * A_BYTES + B_STAGES * B_BYTES;
-    static constexpr int CS = BN >= 128 ? 64 : 32;         // columns of one epilogue step
-    static constexpr int STG_BYTES = kPEpiWarps * 32 * CS * 2;
+    static constexpr int HALVES = BN == 64 ? 1 : 2;        // column parts the epilogue warps share out
+    static constexpr int HALF = BN / HALVES;
+    static constexpr int STEP_BYTES = 32 * 64;             // 32 rows x 32 columns of one warp
+    static constexpr int STG_BYTES = kPEpiWarps * STEP_BYTES * (DX ? 2 : 1);  // d_x: two steps of rows of x
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int SMEM_BYTES = 1024 + RING_BYTES + STG_BYTES + static_cast<int>(sizeof(PairCtl));
     static_assert(A_STAGES <= kMaxStages && B_STAGES <= kMaxStages, "stages");
@@ -177,9 +165,9 @@ struct PairArgs {
     int E, K, H;
     int64_t P;
     void* out;             // [T][H]; d_x: may be NULL (only the weights' gradient)
-    void* scratch;         // [P][H], K > 1
-    int* count;            // [T][NB], zero, K > 1
-    float* dw_part;        // [NB][P], d_x with `other`
+    __half* rows;          // [P][H], K > 1
+    float* scale;          // [P][H / 32], K > 1
+    float* dw_part;        // [parts][P], d_x with `other`
     uint32_t* flags;
 };
 
@@ -188,7 +176,7 @@ struct PairArgs {
 template <typename T, int BN, bool DX>
 __global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
-    using C = PairCfg<BN>;
+    using C = PairCfg<BN, DX>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* aring = smem;
@@ -353,128 +341,136 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
         }
         __syncwarp();
     } else if (warp < kPEpiWarps) {
-        // ---------------- epilogue: this lane's row is 32 (w % 4) + lane; columns of half w / 4
-        constexpr int HALF = BN / 2, CS = C::CS, G = CS / 8;  // G: 16-byte granules of a step's row
+        // ---------------- epilogue: this lane's row is 32 (w % 4) + lane; columns of half w / 4,
+        // 32 a step
+        constexpr int HALF = C::HALF;
         const int q = warp & 3, half = warp >> 2;
-        const uint32_t my = smem_u32(stg + warp * 32 * CS * 2);
+        const uint32_t my = smem_u32(stg + warp * C::STEP_BYTES * (DX ? 2 : 1));
         const int myrow = 32 * q + lane;
-        const int NB = 2 * NT;
+        const int R4 = lane >> 2, j4 = lane & 3;  // row and 16-byte granule of a lane where a warp moves 8 rows
+        const uint32_t swz = (lane >> 1) & 3;     // granule g of row r sits at g ^ ((r >> 1) & 3)
         T* out = static_cast<T*>(A.out);
-        const bool join = K > 1 && out;  // rows of a token are added up
-        T* scratch = static_cast<T*>(A.scratch);
         auto tile_pair = [&](int tile) -> int {
             int e, row0, nrows;
             tile_rows(tile, e, row0, nrows);
             return myrow < nrows ? A.perm[row0 + myrow] : -1;
         };
-        int p_next = static_cast<int>(blockIdx.x) < ntiles ? tile_pair(blockIdx.x) : -1;
+        auto tile_cols = [&](int tile) { return half < C::HALVES ? min(HALF, H - (tile % NT) * BN - half * HALF) : 0; };
+        // d_x: this warp's 32 rows of x, 32 columns from col, into one of its two buffers
+        auto fetch_x = [&](int pair, int col, int buf) {
+            const T* xs = static_cast<const T*>(A.other);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int R = it * 8 + R4;
+                const int pr = __shfl_sync(kFull, pair, R);
+                cp_async_16(my + buf * C::STEP_BYTES + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4),
+                            xs + static_cast<int64_t>(pr < 0 ? 0 : pr / K) * H + col + j4 * 8, pr < 0 ? 0u : 16u);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int tile = blockIdx.x;
+        int p_next = tile < ntiles ? tile_pair(tile) : -1;
+        int buf = 0;
+        if (DX && A.other && tile < ntiles && tile_cols(tile) > 0) fetch_x(p_next, (tile % NT) * BN + half * HALF, 0);
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-            int e, row0, nrows;
-            tile_rows(tile, e, row0, nrows);
-            const int p = p_next;
-            if (tile + static_cast<int>(gridDim.x) < ntiles) p_next = tile_pair(tile + gridDim.x);
+        for (; tile < ntiles; tile += gridDim.x) {
+            const int p = p_next, next_tile = tile + gridDim.x;
             const float w = p >= 0 ? A.weights[p] : 0.0f;
-            const int t = p >= 0 ? p / K : 0;
-            const int nt = tile % NT, col0 = nt * BN + half * HALF;
-            const int ncols = min(HALF, H - col0);  // <= 0: none of this half (the barriers still are)
+            if (next_tile < ntiles) p_next = tile_pair(next_tile);
+            const int nt = tile % NT, col0 = nt * BN + half * HALF, ncols = tile_cols(tile);
+            const int e = span_of(ctl->tstart, A.E, tile / NT);
             if (!mbar_wait(&ctl->tfull[acc], acc_phase, abort, A.flags)) break;
             __syncwarp();
             tc_fence_after();
-            int* count = A.count + static_cast<int64_t>(t) * NB + nt * 2 + half;
-            // every other row of the token is there: add them to this one and write the output
-            const bool last = join && p >= 0 && ncols > 0 && load_acquire(count) == K - 1;
-            const unsigned last_mask = __ballot_sync(kFull, last);
             const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * BN + half * HALF);
             float dot = 0.0f;
-            for (int c = 0; c < ncols; c += CS) {
-#pragma unroll
-                for (int h = 0; h < CS / 32; ++h) {
-                    float v[32];
-                    tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c + 32 * h), v);
-                    const int col = col0 + c + 32 * h;
-                    if (DX) {
-                        if (A.other && p >= 0) {
-                            const T* xr = static_cast<const T*>(A.other) + static_cast<int64_t>(t) * H + col;
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const Chunk<T, 8> xv = *reinterpret_cast<const Chunk<T, 8>*>(xr + 8 * g);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) dot += v[8 * g + i] * to_f(xv.v[i]);
-                            }
-                        }
-                    } else if (A.bias) {
-                        const T* br = static_cast<const T*>(A.bias) + static_cast<int64_t>(e) * H + col;
+            for (int c = 0; c < ncols; c += 32) {
+                float v[32];
+                tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c), v);
+                if (c + 32 >= ncols) {  // the accumulator is read: the next tile may have it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->tempty[acc]);
+                }
+                const int col = col0 + c;
+                const uint32_t stage = my + (DX ? buf * C::STEP_BYTES : 0);
+                if (DX) {
+                    if (A.other) {
+                        // the next step's rows of x (of this tile or the next) on the way, this one's here
+                        const bool more = c + 32 < ncols;
+                        if (more) fetch_x(p, col + 32, buf ^ 1);
+                        else if (next_tile < ntiles && tile_cols(next_tile) > 0)
+                            fetch_x(p_next, (next_tile % NT) * BN + half * HALF, buf ^ 1);
+                        else asm volatile("cp.async.commit_group;" ::: "memory");
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                        __syncwarp();
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
-                            const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br + 8 * g);
+                            const uint4 raw = ld_shared_u4(stage + lane * 64 + ((g ^ swz) << 4));
+                            const T* xv = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) v[8 * g + i] += to_f(bv.v[i]);
+                            for (int i = 0; i < 8; ++i) dot += v[8 * g + i] * to_f(xv[i]);
                         }
                     }
+                    buf ^= 1;
+                    if (!out) {
+                        __syncwarp();
+                        continue;
+                    }
+                } else if (A.bias) {
+                    const T* br = static_cast<const T*>(A.bias) + static_cast<int64_t>(e) * H + col;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        float s[8];
+                        const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br + 8 * g);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) s[i] = v[8 * g + i] * w;  // rounded once to T below
-                        const int gg = 4 * h + g;
-                        st_shared_u4(my + lane * CS * 2 + ((gg ^ (lane & (G - 1))) << 4), pack8<T>(s));
+                        for (int i = 0; i < 8; ++i) v[8 * g + i] += to_f(bv.v[i]);
                     }
                 }
-                if (DX && !out) continue;
-                __syncwarp();
-                constexpr int RPI = 32 / G;  // rows one warp instruction covers
+                float f = w;
+                if (K > 1) {
+                    float m = 0.0f;
 #pragma unroll
-                for (int it = 0; it < 32 / RPI; ++it) {
-                    const int R = it * RPI + lane / G, j = lane % G;
-                    const uint4 val = ld_shared_u4(my + R * CS * 2 + ((j ^ (R & (G - 1))) << 4));
+                    for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
+                    // exponent of the largest |v w|, 40 at least: fp16's last step is then 2^-125
+                    const int ex = max(static_cast<int>((__float_as_uint(m * fabsf(w)) >> 23) & 255), 40);
+                    f = w * __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+                    f = fminf(fmaxf(f, -3e38f), 3e38f);  // only where |v w| is below 2^-87
+                    if (p >= 0) A.scale[static_cast<int64_t>(p) * (H / 32) + (col >> 5)] = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+                }
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float s[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[i] = v[8 * g + i] * f;
+                    st_shared_u4(stage + lane * 64 + ((g ^ swz) << 4), K > 1 ? pack8<__half>(s) : pack8<T>(s));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int R = it * 8 + R4;
+                    const uint4 val = ld_shared_u4(stage + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4));
                     const int pr = __shfl_sync(kFull, p, R);
-                    if (pr < 0) continue;
-                    const int64_t col = col0 + c + j * 8;
-                    if (K == 1) {
-                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(pr) * H + col) = val;
-                    } else if (!((last_mask >> R) & 1u)) {
-                        *reinterpret_cast<uint4*>(scratch + static_cast<int64_t>(pr) * H + col) = val;
-                    } else {
-                        const int tr = pr / K, kr = pr - tr * K;
-                        float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                        for (int k = 0; k < K; ++k)
-                            add8<T>(s, k == kr ? val : ldcg_u4(scratch + (static_cast<int64_t>(tr) * K + k) * H + col));
-                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(tr) * H + col) = pack8<T>(s);
+                    const int64_t at = static_cast<int64_t>(pr) * H + col + j4 * 8;
+                    if (pr >= 0) {
+                        if (K > 1) *reinterpret_cast<uint4*>(A.rows + at) = val;
+                        else *reinterpret_cast<uint4*>(out + at) = val;
                     }
                 }
                 __syncwarp();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->tempty[acc]);
+            if (ncols <= 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->tempty[acc]);
+                if (DX && A.other && next_tile < ntiles && tile_cols(next_tile) > 0)
+                    fetch_x(p_next, (next_tile % NT) * BN + half * HALF, buf);
+            }
+            if (DX && A.other && p >= 0 && half < C::HALVES)
+                A.dw_part[static_cast<int64_t>(nt * C::HALVES + half) * A.P + p] = dot;
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1;
-            if (DX && A.other && p >= 0) A.dw_part[static_cast<int64_t>(nt * 2 + half) * A.P + p] = dot;
-            if (join && ncols > 0) {
-                // the rows stored above are visible before they are counted
-                __threadfence();
-                __syncwarp();
-                const bool late = p >= 0 && !last && atomicAdd(count, 1) == K - 1;
-                unsigned todo = __ballot_sync(kFull, late);
-                if (todo) {
-                    __threadfence();
-                    __syncwarp();
-                }
-                while (todo) {  // the other rows came in meanwhile: add all K from memory
-                    const int R = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    const int tr = __shfl_sync(kFull, t, R);
-                    for (int j = lane * 8; j < ncols; j += 32 * 8) {
-                        float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                        for (int k = 0; k < K; ++k)
-                            add8<T>(s, ldcg_u4(scratch + (static_cast<int64_t>(tr) * K + k) * H + col0 + j));
-                        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(tr) * H + col0 + j) = pack8<T>(s);
-                    }
-                }
-            }
         }
+        if (DX) asm volatile("cp.async.wait_all;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -484,62 +480,109 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
     }
 }
 
-// ---------------------------------------------------------------- d_w
-// One warp per token: d_w = sum of the column parts of x . (W_e^T g), plus g . b_e.
-template <typename T>
-__global__ void __launch_bounds__(256)
-dweights_kernel(const float* __restrict__ dw_part, int nparts, const T* __restrict__ g, const T* __restrict__ bias,
-                const int32_t* __restrict__ expert_idx, int64_t T_, int K, int H, float* __restrict__ d_weights) {
+// ---------------------------------------------------------------- join
+struct JoinArgs {
+    const __half* rows;    // [P][H]
+    const float* scale;    // [P][H / 32]
+    void* out;             // [T][H], or NULL
+    const float* dw_part;  // [parts][P]; d_weights only
+    int parts;
+    const void* g;         // [T][H], with bias
+    const void* bias;      // [E][H] or NULL
+    const int32_t* expert_idx;
+    float* d_weights;      // [P] or NULL
+    int64_t T;
+    int K, H;
+};
+
+// LPT lanes per token, 8 columns each at a time; KM: an upper bound of K.
+template <typename T, int KM>
+__global__ void __launch_bounds__(256) join_kernel(const JoinArgs A, int LPT) {
     griddep_wait();  // every global access below comes after the previous grid
-    const int lane = threadIdx.x & 31;
-    const int64_t P = T_ * K;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T_; t += static_cast<int64_t>(gridDim.x) * 8) {
-        for (int k = 0; k < K; ++k) {
-            const int64_t p = t * K + k;
-            float s = 0.0f;
-            if (bias) {
-                const T* br = bias + static_cast<int64_t>(expert_idx[p]) * H;
-                for (int c = lane * 8; c < H; c += 256) {
-                    const Chunk<T, 8> gv = *reinterpret_cast<const Chunk<T, 8>*>(g + t * H + c);
-                    const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br + c);
+    const int lane = threadIdx.x & 31, sub = lane % LPT, K = A.K, H = A.H;
+    const int64_t P = A.T * K;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * (32 / LPT);
+    // a warp's tokens run in step: lanes past the last token only take part in the shuffles
+    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (32 / LPT); base < A.T; base += step) {
+        const int64_t t = base + lane / LPT;
+        const bool valid = t < A.T;
+        float dot[KM];
+        const T* br[KM];
+        const bool with_bias = A.d_weights && A.bias;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s += to_f(gv.v[i]) * to_f(bv.v[i]);
+        for (int k = 0; k < KM; ++k) {
+            dot[k] = 0.0f;
+            br[k] = with_bias && valid && k < K ? static_cast<const T*>(A.bias) + static_cast<int64_t>(A.expert_idx[t * K + k]) * H : nullptr;
+        }
+        for (int c = sub * 8; valid && c < H; c += LPT * 8) {
+            if (A.out) {
+                Chunk<__half, 8> r[KM];
+                float f[KM];
+#pragma unroll
+                for (int k = 0; k < KM; ++k)
+                    if (k < K) {
+                        r[k] = *reinterpret_cast<const Chunk<__half, 8>*>(A.rows + (t * K + k) * H + c);
+                        f[k] = A.scale[(t * K + k) * (H / 32) + (c >> 5)];
+                    }
+                float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < KM; ++k)
+                    if (k < K)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s[i] = fmaf(to_f(r[k].v[i]), f[k], s[i]);
+                *reinterpret_cast<uint4*>(static_cast<T*>(A.out) + t * H + c) = pack8<T>(s);
+            }
+            if (with_bias) {
+                const Chunk<T, 8> gv = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.g) + t * H + c);
+#pragma unroll
+                for (int k = 0; k < KM; ++k)
+                    if (k < K) {
+                        const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br[k] + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dot[k] += to_f(gv.v[i]) * to_f(bv.v[i]);
+                    }
+            }
+        }
+        if (A.d_weights) {
+#pragma unroll
+            for (int k = 0; k < KM; ++k) {
+                if (k < K) {
+                    if (valid)
+                        for (int i = sub; i < A.parts; i += LPT) dot[k] += A.dw_part[i * P + t * K + k];
+                    for (int off = LPT / 2; off >= 1; off >>= 1) dot[k] += __shfl_xor_sync(kFull, dot[k], off);
+                    if (valid && sub == 0) A.d_weights[t * K + k] = dot[k];
                 }
             }
-            for (int i = lane; i < nparts; i += 32) s += dw_part[i * P + p];
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
-            if (lane == 0) d_weights[p] = s;
         }
     }
 }
 
 // ---------------------------------------------------------------- dW and db
-// Warps 0-7 epilogue, 8-11 rows of g (scaled), 12-15 rows of x, 16 MMA issuer.
-constexpr int kWThreads = 544;
-constexpr int kWG0 = 256, kWX0 = 384, kWMmaWarp = 16;
+// Warps 0-7 scale the rows of g and drain the sums, 8-11 gather, 12 issues the MMAs.
+constexpr int kWThreads = 416;
+constexpr int kWGather0 = 8, kWMmaWarp = 12;
+
+struct WCfg {
+    static constexpr int KT = 32;              // pairs per stage
+    static constexpr int GROUP = KT * 128;     // 64 columns of a stage's rows
+    static constexpr int OP = 4 * GROUP;       // 256 columns
+    static constexpr int STAGE = 2 * OP;       // g then x: 32 KiB
+    static constexpr int STAGES = 6;
+    static constexpr int STG = 8 * 32 * 64;    // staging: 32 rows x 64 bytes a warp
+};
 
 struct __align__(8) WCtl {
-    uint64_t full[4], empty[4];
+    uint64_t raw[WCfg::STAGES], full[WCfg::STAGES], empty[WCfg::STAGES];
     uint64_t tfull, tempty;
     uint32_t tmem_base;
     int abort;
     int off[kMaxE + 1];
     int pstart[kMaxE + 1];  // first piece of each expert
     int sstart[kMaxE + 1];  // first slot of each expert (experts of two pieces or more)
-    float db[4][32][8];
+    float db[8][32][8];
 };
-
-struct WCfg {
-    static constexpr int KT = 64;                   // pairs per stage
-    static constexpr int GROUP = KT * 128;          // 64 columns of a stage's rows
-    static constexpr int OP = 4 * GROUP;            // 256 columns
-    static constexpr int STAGE = 2 * OP;            // g then x: 64 KiB
-    static constexpr int STAGES = 3;
-    static constexpr int STG = 8 * 32 * 64;         // epilogue staging: 32 rows x 64 bytes a warp
-    static constexpr int SMEM = 1024 + STAGES * STAGE + STG + static_cast<int>(sizeof(WCtl));
-    static_assert(SMEM <= 227 * 1024, "shared memory");
-};
+constexpr int kWSmem = 1024 + WCfg::STAGES * WCfg::STAGE + WCfg::STG + static_cast<int>(sizeof(WCtl));
+static_assert(kWSmem <= 227 * 1024, "shared memory");
 
 struct WgradArgs {
     const void* x;
@@ -581,8 +624,9 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
     const int H = A.H, K = A.K;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&ctl->full[s], 256);  // 128 threads store g, 128 gather x
-            mbar_init(&ctl->empty[s], 1);   // tcgen05.commit
+            mbar_init(&ctl->raw[s], 128);  // the gather threads' copies
+            mbar_init(&ctl->full[s], 8);   // the scaling warps
+            mbar_init(&ctl->empty[s], 1);  // tcgen05.commit
         }
         mbar_init(&ctl->tfull, 1);
         mbar_init(&ctl->tempty, 8);
@@ -618,114 +662,38 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         return r;
     };
 
-    if (warp >= kWG0 / 32 && warp < kWG0 / 32 + 4) {
-        // ---------------- rows of g, scaled: a lane has 8 fixed columns, 32 / lanes rows a pass
+    if (warp >= kWGather0 && warp < kWGather0 + 4) {
+        // ---------------- gather: rows of g and x as they are, MN-major; a warp moves a row of 256
+        // columns at a time; rows past the piece's end are zeros
         const T* g = static_cast<const T*>(A.g);
-        const int w4 = warp - kWG0 / 32;
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
-            const Unit r = unit_of(u);
-            const int cols = min(kWTile, H - r.o0);
-            const bool on = lane * 8 < cols;
-            float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            const uint32_t dst0 = (lane >> 3) * C::GROUP;
-            // this warp's 16 rows of a stage are w4, w4 + 4, ...; lane i < 16 looks row i up
-            auto look = [&](int p0, int& tok, float& wt) {
-                const int i = p0 + w4 + 4 * (lane & 15);
-                const int p = i < r.hi ? A.perm[i] : -1;
-                tok = p >= 0 ? p / K : -1;
-                wt = p >= 0 ? A.weights[p] : 0.0f;
-            };
-            int tok, ntok;
-            float wt, nwt;
-            look(r.lo, tok, wt);
-            for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
-                look(p0 + C::KT, ntok, nwt);
-                if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
-                const uint32_t base = smem_u32(smem + stage * C::STAGE) + dst0;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    Chunk<T, 8> v[8];
-                    float wr[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int tr = __shfl_sync(kFull, tok, b * 8 + i);
-                        wr[i] = __shfl_sync(kFull, wt, b * 8 + i);
-                        if (tr >= 0 && on) v[i] = *reinterpret_cast<const Chunk<T, 8>*>(g + static_cast<int64_t>(tr) * H + r.o0 + lane * 8);
-                        else wr[i] = 0.0f, v[i] = Chunk<T, 8>{};
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = w4 + 4 * (b * 8 + i);
-                        float s[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            s[j] = wr[i] * to_f(v[i].v[j]);
-                            db[j] += s[j];
-                        }
-                        if (on) st_shared_u4(base + row * 128 + (((lane & 7) ^ (row & 7)) << 4), pack8<T>(s));
-                    }
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&ctl->full[stage]);
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-                tok = ntok;
-                wt = nwt;
-            }
-            if (ok && A.db && r.i0 == 0) {
-                // the four warps' sums, in order
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ctl->db[w4][lane][j] = db[j];
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (w4 == 0 && on) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) db[j] = ((ctl->db[0][lane][j] + ctl->db[1][lane][j]) + ctl->db[2][lane][j]) + ctl->db[3][lane][j];
-                    const int o = r.o0 + lane * 8;
-                    if (r.pieces == 1) {
-                        *reinterpret_cast<uint4*>(static_cast<T*>(A.db) + static_cast<int64_t>(r.e) * H + o) = pack8<T>(db);
-                    } else {
-                        float* d = A.part_db + (static_cast<int64_t>(ctl->sstart[r.e]) + r.piece) * H + o;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) d[j] = db[j];
-                    }
-                }
-            }
-        }
-    } else if (warp >= kWX0 / 32 && warp < kWX0 / 32 + 4) {
-        // ---------------- rows of x
         const T* x = static_cast<const T*>(A.x);
-        const int w4 = warp - kWX0 / 32;
+        const int w4 = warp - kWGather0;
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
             const Unit r = unit_of(u);
-            const bool on = lane * 8 < min(kWTile, H - r.i0);
-            const uint32_t dst0 = C::OP + (lane >> 3) * C::GROUP;
+            const bool on_g = lane * 8 < min(kWTile, H - r.o0), on_x = lane * 8 < min(kWTile, H - r.i0);
+            // this warp's 8 rows of a stage are w4, w4 + 4, ...; lane i < 8 looks row i up, a stage ahead
             auto look = [&](int p0) {
-                const int i = p0 + w4 + 4 * (lane & 15);
+                const int i = p0 + w4 + 4 * (lane & 7);
                 return i < r.hi ? A.perm[i] / K : -1;
             };
             int tok = look(r.lo);
             for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
                 const int ntok = look(p0 + C::KT);
                 if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
-                const uint32_t base = smem_u32(smem + stage * C::STAGE) + dst0;
+                const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const int row = w4 + 4 * i;
                     const int tr = __shfl_sync(kFull, tok, i);
-                    if (on)
-                        cp_async_16(base + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
-                                    x + static_cast<int64_t>(tr < 0 ? 0 : tr) * H + r.i0 + lane * 8, tr < 0 ? 0u : 16u);
+                    const uint32_t at = base + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+                    const int64_t src = static_cast<int64_t>(tr < 0 ? 0 : tr) * H + lane * 8;
+                    if (on_g) cp_async_16(at, g + src + r.o0, tr < 0 ? 0u : 16u);
+                    if (on_x) cp_async_16(at + C::OP, x + src + r.i0, tr < 0 ? 0u : 16u);
                 }
-                cp_async_arrive_noinc(&ctl->full[stage]);
+                cp_async_arrive_noinc(&ctl->raw[stage]);
                 if (++stage == C::STAGES) {
                     stage = 0;
                     phase ^= 1;
@@ -751,7 +719,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                     tc_fence_after();
                     const uint32_t g_addr = smem_u32(smem + stage * C::STAGE), x_addr = g_addr + C::OP;
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
+                    for (int ks = 0; ks < C::KT / 16; ++ks)
                         for (int mh = 0; mh < halves; ++mh)
                             mma_f16(tmem + static_cast<uint32_t>(mh * 256), mn_desc(g_addr + mh * 2 * C::GROUP + ks * 2048, C::GROUP),
                                     mn_desc(x_addr + ks * 2048, C::GROUP), idesc, (p0 != r.lo || ks != 0) ? 1u : 0u);
@@ -768,17 +736,83 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         }
         __syncwarp();
     } else if (warp < 8) {
-        // ---------------- epilogue: rows 32 (w % 4) + lane of each half, columns of half w / 4
+        // ---------------- scale the staged rows of g in place (db on the way), then drain dW: rows
+        // 32 (w % 4) + lane of each half, columns of half w / 4
         const int q = warp & 3, ch = warp >> 2;
         const uint32_t my = smem_u32(stg + warp * 32 * 64);
-        uint32_t acc_phase = 0;
+        int stage = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
         T* dW = static_cast<T*>(A.dW);
         for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
             const Unit r = unit_of(u);
+            const int rows = min(kWTile, H - r.o0), cols = min(kWTile, H - r.i0);
+            const bool on = lane * 8 < rows;
+            float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            // weights of a stage's rows warp, warp + 8, ...: lane i < 4 looks row i up; the pair's number
+            // two stages ahead, its weight one
+            auto pair_at = [&](int p0) {
+                const int i = p0 + warp + 8 * (lane & 3);
+                return i < r.hi ? A.perm[i] : -1;
+            };
+            auto weight_of = [&](int p) { return p >= 0 ? A.weights[p] : 0.0f; };
+            float wt = weight_of(pair_at(r.lo));
+            int np = pair_at(r.lo + C::KT);
+            for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
+                const float nwt = weight_of(np);
+                np = pair_at(p0 + 2 * C::KT);
+                if (!(ok = mbar_wait(&ctl->raw[stage], phase, abort, A.flags))) break;
+                const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = warp + 8 * i;
+                    const float wr = __shfl_sync(kFull, wt, i);
+                    const uint32_t at = base + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+                    if (on) {
+                        const uint4 raw = ld_shared_u4(at);
+                        const T* v = reinterpret_cast<const T*>(&raw);
+                        float s[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            s[j] = wr * to_f(v[j]);
+                            db[j] += s[j];
+                        }
+                        st_shared_u4(at, pack8<T>(s));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->full[stage]);
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                wt = nwt;
+            }
+            if (!ok) break;
+            if (A.db && r.i0 == 0) {
+                // the eight warps' sums, in order
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ctl->db[warp][lane][j] = db[j];
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (warp == 0 && on) {
+                    for (int k = 1; k < 8; ++k)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) db[j] += ctl->db[k][lane][j];
+                    const int o = r.o0 + lane * 8;
+                    if (r.pieces == 1) {
+                        *reinterpret_cast<uint4*>(static_cast<T*>(A.db) + static_cast<int64_t>(r.e) * H + o) = pack8<T>(db);
+                    } else {
+                        float* d = A.part_db + (static_cast<int64_t>(ctl->sstart[r.e]) + r.piece) * H + o;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d[j] = db[j];
+                    }
+                }
+            }
             if (!mbar_wait(&ctl->tfull, acc_phase, abort, A.flags)) break;
             __syncwarp();
             tc_fence_after();
-            const int rows = min(kWTile, H - r.o0), cols = min(kWTile, H - r.i0);
             for (int mh = 0; mh < (rows + 127) / 128 && dW; ++mh) {
                 const int o_first = mh * 128 + 32 * q;
                 if (o_first >= rows) break;  // rows is a multiple of 64, so a warp's 32 are in or out together
@@ -846,6 +880,7 @@ __global__ void __launch_bounds__(256) wgrad_sum_kernel(const WgradArgs A) {
     griddep_wait();  // every global access below comes after the previous grid
     __shared__ struct {
         int off[kMaxE + 1], pstart[kMaxE + 1], sstart[kMaxE + 1];
+        float4 sum[256];
     } s;
     const int e = blockIdx.y, H = A.H;
     const int n = A.offsets[e + 1] - A.offsets[e];
@@ -860,23 +895,42 @@ __global__ void __launch_bounds__(256) wgrad_sum_kernel(const WgradArgs A) {
         slot = s.sstart[e];
     }
     const int64_t nW = static_cast<int64_t>(H) * H;
+    // G threads share four elements: each adds pieces g, g + G, ... in order, then the G sums in order
+    int G = 1;
+    while (G < 8 && G < pieces) G *= 2;
+    const int per = 256 / G, g = threadIdx.x / per, at = threadIdx.x % per;
     auto add = [&](const float* part, int64_t stride, T* out, int64_t count) {
-        for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < count; i += static_cast<int64_t>(gridDim.x) * 1024) {
+        for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * per * 4; i0 < count; i0 += static_cast<int64_t>(gridDim.x) * per * 4) {
+            const int64_t i = i0 + at * 4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < count) {
 #pragma unroll 4
-            for (int j = 0; j < pieces; ++j) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(part + (slot + j) * stride + i));
-                a.x += v.x;
-                a.y += v.y;
-                a.z += v.z;
-                a.w += v.w;
+                for (int j = g; j < pieces; j += G) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(part + (slot + j) * stride + i));
+                    a.x += v.x;
+                    a.y += v.y;
+                    a.z += v.z;
+                    a.w += v.w;
+                }
             }
-            Chunk<T, 4> o;
-            o.v[0] = from_f<T>(a.x);
-            o.v[1] = from_f<T>(a.y);
-            o.v[2] = from_f<T>(a.z);
-            o.v[3] = from_f<T>(a.w);
-            *reinterpret_cast<Chunk<T, 4>*>(out + i) = o;
+            s.sum[threadIdx.x] = a;
+            __syncthreads();
+            if (g == 0 && i < count) {
+                for (int k = 1; k < G; ++k) {
+                    const float4 v = s.sum[k * per + at];
+                    a.x += v.x;
+                    a.y += v.y;
+                    a.z += v.z;
+                    a.w += v.w;
+                }
+                Chunk<T, 4> o;
+                o.v[0] = from_f<T>(a.x);
+                o.v[1] = from_f<T>(a.y);
+                o.v[2] = from_f<T>(a.z);
+                o.v[3] = from_f<T>(a.w);
+                *reinterpret_cast<Chunk<T, 4>*>(out + i) = o;
+            }
+            __syncthreads();
         }
     };
     if (A.dW) add(A.part, nW, static_cast<T*>(A.dW) + e * nW, nW);
@@ -897,16 +951,17 @@ bool weight_map(CUtensorMap* map, const void* W, moe_dtype_t dtype, uint64_t row
 }
 
 template <typename T, int BN, bool DX>
-cudaError_t pair_launch(const void* W, moe_dtype_t dtype, const PairArgs& a, int sms, cudaStream_t s) {
+cudaError_t pair_launch(const void* W, moe_dtype_t dtype, const PairArgs& a, int sms, cudaStream_t s, int* parts) {
+    using C = PairCfg<BN, DX>;
     CUtensorMap map;
     if (!weight_map(&map, W, dtype, static_cast<uint64_t>(a.E) * a.H, a.H, DX ? 64 : BN)) return cudaErrorInvalidValue;
     auto kernel = pair_kernel<T, BN, DX>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg<BN>::SMEM_BYTES);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    const int64_t hit = a.P < a.E ? a.P : a.E;
-    const int64_t tiles = (a.P / 128 + hit) * ((a.H + BN - 1) / BN);
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kPairThreads),
-                      PairCfg<BN>::SMEM_BYTES, s, map, a);
+    const int nt = (a.H + BN - 1) / BN;
+    *parts = nt * C::HALVES;
+    const int64_t tiles = (a.P / 128 + (a.P < a.E ? a.P : a.E)) * nt;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kPairThreads), C::SMEM_BYTES, s, map, a);
 }
 
 // Columns per tile: 256 where that leaves a tile for every SM, narrower ones for few pairs.
@@ -920,26 +975,48 @@ int tile_columns(int64_t P, int E, int H, int sms) {
 template <typename T, bool DX>
 cudaError_t pair_width(const void* W, moe_dtype_t dtype, const PairArgs& a, int sms, cudaStream_t s, int* parts) {
     const int bn = tile_columns(a.P, a.E, a.H, sms);
-    *parts = 2 * ((a.H + bn - 1) / bn);
-    if (a.K > 1 && a.out) {  // the parts that are there, none yet
-        cudaError_t e = cudaMemsetAsync(a.count, 0, sizeof(int) * (a.P / a.K) * *parts, s);
-        if (e != cudaSuccess) return e;
-    }
-    if (bn == 256) return pair_launch<T, 256, DX>(W, dtype, a, sms, s);
-    if (bn == 128) return pair_launch<T, 128, DX>(W, dtype, a, sms, s);
-    return pair_launch<T, 64, DX>(W, dtype, a, sms, s);
+    if (bn == 256) return pair_launch<T, 256, DX>(W, dtype, a, sms, s, parts);
+    if (bn == 128) return pair_launch<T, 128, DX>(W, dtype, a, sms, s, parts);
+    return pair_launch<T, 64, DX>(W, dtype, a, sms, s, parts);
+}
+
+template <typename T>
+cudaError_t join_launch(const JoinArgs& a, int sms, cudaStream_t s) {
+    int lpt = 8;
+    while (lpt < 32 && lpt * 8 < a.H) lpt *= 2;
+    const int64_t tokens = 8 * (32 / lpt), want = (a.T + tokens - 1) / tokens, cap = static_cast<int64_t>(sms) * 16;
+    const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
+    if (a.K <= 2) return launch_pdl(join_kernel<T, 2>, grid, dim3(256), 0, s, a, lpt);
+    if (a.K <= 4) return launch_pdl(join_kernel<T, 4>, grid, dim3(256), 0, s, a, lpt);
+    if (a.K <= 8) return launch_pdl(join_kernel<T, 8>, grid, dim3(256), 0, s, a, lpt);
+    return launch_pdl(join_kernel<T, 16>, grid, dim3(256), 0, s, a, lpt);
+}
+
+template <typename T>
+cudaError_t fwd_type(const void* W, moe_dtype_t dtype, const PairArgs& a, int64_t T_, int sms, cudaStream_t s) {
+    int parts = 0;
+    cudaError_t e = pair_width<T, false>(W, dtype, a, sms, s, &parts);
+    if (e != cudaSuccess || a.K == 1) return e;
+    JoinArgs j{};
+    j.rows = a.rows;
+    j.scale = a.scale;
+    j.out = a.out;
+    j.T = T_;
+    j.K = a.K;
+    j.H = a.H;
+    return join_launch<T>(j, sms, s);
 }
 
 template <typename T>
 cudaError_t wgrad_launch(const WgradArgs& a, int sms, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, WCfg::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
     if (e != cudaSuccess) return e;
     const int64_t hit = a.P < a.E ? a.P : a.E;
     const int64_t units = (hit + a.extra) * wgrad_tiles(a.H);
-    e = launch_pdl(wgrad_kernel<T>, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kWThreads), WCfg::SMEM, s, a);
+    e = launch_pdl(wgrad_kernel<T>, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kWThreads), kWSmem, s, a);
     if (e != cudaSuccess) return e;
-    int x = (a.H * a.H + 4095) / 4096;
-    if (x > 64) x = 64;
+    int x = a.H * a.H / 256;
+    if (x > 256) x = 256;
     return launch_pdl(wgrad_sum_kernel<T>, dim3(x, a.E), dim3(256), 0, s, a);
 }
 
@@ -960,11 +1037,21 @@ cudaError_t bwd_type(const void* W, const void* bias, moe_dtype_t dtype, PairArg
     if (a.out || d_weights) {
         int parts = 0;
         e = pair_width<T, true>(W, dtype, a, sms, s, &parts);
-        if (e == cudaSuccess && d_weights) {
-            const int64_t want = (T_ + 7) / 8, cap = static_cast<int64_t>(sms) * 8;
-            e = launch_pdl(dweights_kernel<T>, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s,
-                           static_cast<const float*>(a.dw_part), parts, static_cast<const T*>(a.src),
-                           static_cast<const T*>(bias), expert_idx, T_, a.K, a.H, d_weights);
+        if (e == cudaSuccess && (d_weights || a.K > 1)) {
+            JoinArgs j{};
+            j.rows = a.rows;
+            j.scale = a.scale;
+            j.out = a.K > 1 ? a.out : nullptr;
+            j.dw_part = a.dw_part;
+            j.parts = parts;
+            j.g = a.src;
+            j.bias = bias;
+            j.expert_idx = expert_idx;
+            j.d_weights = d_weights;
+            j.T = T_;
+            j.K = a.K;
+            j.H = a.H;
+            e = join_launch<T>(j, sms, s);
         }
     }
     if (e == cudaSuccess && (wg.dW || wg.db)) e = wgrad_launch<T>(wg, sms, s);
@@ -1004,7 +1091,7 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
     if (!workspace) return MOE_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return MOE_ERR_MISALIGNED;
     if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
-    int sms = 0, parts = 0;
+    int sms = 0;
     if (device_sms(&sms) != cudaSuccess) return MOE_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PairArgs a{};
@@ -1018,12 +1105,12 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
     a.H = H;
     a.P = static_cast<int64_t>(P);
     a.out = y;
-    a.scratch = ws + L.scratch;
-    a.count = reinterpret_cast<int*>(ws + L.count);
+    a.rows = reinterpret_cast<__half*>(ws + L.rows);
+    a.scale = reinterpret_cast<float*>(ws + L.scale);
     a.flags = reinterpret_cast<uint32_t*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(dtype == MOE_DTYPE_BF16 ? pair_width<__nv_bfloat16, false>(W, dtype, a, sms, s, &parts)
-                                               : pair_width<__half, false>(W, dtype, a, sms, s, &parts));
+    return cuda_status(dtype == MOE_DTYPE_BF16 ? fwd_type<__nv_bfloat16>(W, dtype, a, T, sms, s)
+                                               : fwd_type<__half>(W, dtype, a, T, sms, s));
 }
 
 moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dtype_t dtype, const void* d_out,
@@ -1074,8 +1161,8 @@ moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dt
     a.H = H;
     a.P = static_cast<int64_t>(P);
     a.out = d_x;
-    a.scratch = ws + L.scratch;
-    a.count = reinterpret_cast<int*>(ws + L.count);
+    a.rows = reinterpret_cast<__half*>(ws + L.rows);
+    a.scale = reinterpret_cast<float*>(ws + L.scale);
     a.dw_part = reinterpret_cast<float*>(ws + L.dw_part);
     a.flags = reinterpret_cast<uint32_t*>(ws);
     WgradArgs g{};

@@ -21,14 +21,12 @@ inline int wgrad_tiles(int H) {
     const int n = (H + kWTile - 1) / kWTile;
     return n * n;
 }
-// Pieces beyond one per expert that all experts share in proportion to their pairs:
-// enough to fill the GPU once where the experts' tiles alone do not, else two for every
-// three experts, so that an expert with 1.5 times its share is cut and others are not.
+// Pieces beyond one per expert that the experts share in proportion to their pairs: with
+// few tiles as many as fill the GPU once; with more tiles than SMs an expert is cut where
+// its tiles alone would take a block longer than an even share of all the work.
 inline int wgrad_extra(int E, int H) {
-    const int tiles = wgrad_tiles(H);
-    if (E * tiles >= kWUnits) return (2 * E + 2) / 3;
-    const int fill = kWUnits / tiles - E;
-    return fill > 0 ? fill : 0;
+    const int tiles = wgrad_tiles(H), fill = kWUnits / tiles;
+    return E * tiles >= kWUnits ? fill : fill - E > 0 ? fill - E : 0;
 }
 // Pieces of an expert with n of the P pairs: at most E + extra in all.
 __host__ __device__ inline int wgrad_pieces(int n, int64_t P, int extra) {
@@ -40,9 +38,9 @@ __host__ __device__ inline int wgrad_pieces(int n, int64_t P, int extra) {
 }
 
 struct ExpertsWs {
-    size_t count = 0;    // int32 [T][2 * ceil(H / 64)]: finished parts of every token's columns
-    size_t scratch = 0;  // elements [T * K][H]: the pairs' rows, K > 1
-    size_t dw_part = 0;  // float [2 * ceil(H / 64)][T * K]
+    size_t rows = 0;     // fp16 [T * K][H]: the pairs' rows, K > 1
+    size_t scale = 0;    // float [T * K][H / 32]: their factors, K > 1
+    size_t dw_part = 0;  // float [ceil(H / 64) + 1][T * K]: column parts of the weights' gradient
     size_t part = 0;     // float [2 * extra][H][H]
     size_t part_db = 0;  // float [2 * extra][H]
     size_t total = 0;
@@ -50,7 +48,7 @@ struct ExpertsWs {
 
 inline ExpertsWs experts_ws(int64_t T, int E, int K, int H, size_t begin) {
     ExpertsWs L;
-    const size_t P = static_cast<size_t>(T) * K, nb = 2 * static_cast<size_t>((H + 63) / 64);
+    const size_t P = static_cast<size_t>(T) * K, nb = static_cast<size_t>((H + 63) / 64 + 1);
     const size_t slots = 2 * static_cast<size_t>(wgrad_extra(E, H));
     size_t off = align_up(begin, 256);
     auto take = [&](size_t bytes) {
@@ -58,8 +56,8 @@ inline ExpertsWs experts_ws(int64_t T, int E, int K, int H, size_t begin) {
         off = align_up(off + bytes, 256);
         return at;
     };
-    L.count = take(K > 1 ? sizeof(int32_t) * T * nb : 0);
-    L.scratch = take(K > 1 ? 2 * P * H : 0);
+    L.rows = take(K > 1 ? 2 * P * H : 0);
+    L.scale = take(K > 1 ? sizeof(float) * P * (H / 32) : 0);
     L.dw_part = take(sizeof(float) * nb * P);
     L.part = take(sizeof(float) * slots * H * H);
     L.part_db = take(sizeof(float) * slots * H);
