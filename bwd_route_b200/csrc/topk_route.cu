@@ -13,12 +13,13 @@
 // fp32, and where two neighbours in the result lie within the error of that
 // computation the warp repeats the choice in fp64; about 1 % of the warps do.
 //
-// A token belongs to LPT lanes with VPL consecutive experts each, so a warp works on
-// 32 / LPT tokens at once: K rounds of a local maximum, a shuffle maximum over the
-// lanes and a ballot, whose lowest lane holds the lowest index. The block counts its
-// pairs per expert in shared memory; a second kernel turns the blocks' counts into
-// each block's base positions, a third writes the lists (stable, as in route.cu).
-// Few tokens take one launch of one block that does all three.
+// A token belongs to LPT lanes with VPL consecutive experts each. Up to 64 experts a
+// warp works on 32 / LPT tokens at once: K rounds of a local maximum, a shuffle maximum
+// over the lanes and a ballot, whose lowest lane holds the lowest index. Above, a warp
+// takes one token and finds the K largest through a threshold (choose_by_threshold). The
+// block counts its pairs per expert in shared memory; a second kernel turns the blocks'
+// counts into each block's base positions, a third writes the lists (stable, as in
+// route.cu). Few tokens take one launch of one block that does all three.
 #include <cmath>
 #include <cstdint>
 
@@ -97,7 +98,7 @@ __device__ __forceinline__ V lanes_sum(V v) {
 // ---------------------------------------------------------------- one token's row
 template <typename T, int VPL>
 __device__ __forceinline__ void load_logits(const T* row, int e0, int E, bool vec, bool valid, float (&l)[VPL]) {
-    constexpr int C = 16 / sizeof(T);
+    constexpr int C = VPL * sizeof(T) < 16 ? VPL : 16 / sizeof(T);
     static_assert(VPL % C == 0, "whole chunks");
     if (vec) {
 #pragma unroll
@@ -148,6 +149,76 @@ struct WarpSmem {
 __device__ __forceinline__ int pad_e(int e) { return e + (e >> 5); }
 __host__ __device__ constexpr int padded(int ep) { return ep + ep / 32 + 1; }
 
+// The groups that stay, through shared memory: bit g of kept. Returns whether fp32 leaves
+// that open.
+template <typename V, int LPT, int VPL, bool SCORES>
+__device__ __forceinline__ bool group_kept(const V (&v)[VPL], int e0, int tok, const Rule& R, V* vals, V* gscores, float tol,
+                                           unsigned& kept) {
+    constexpr unsigned kMine = LPT == 32 ? kFull : (1u << (LPT & 31)) - 1u;
+    const int sub = (threadIdx.x & 31) % LPT;
+    V* val = vals + tok * padded(LPT * VPL);
+    V* gs = gscores + tok * R.G;
+    bool unsure = false;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) val[pad_e(e0 + j)] = v[j];
+    __syncwarp();
+    for (int g = sub; g < R.G; g += LPT) {
+        V a = -INFINITY, b = -INFINITY;
+        for (int i = 0; i < R.S; ++i) {
+            const V x = val[pad_e(g * R.S + i)];
+            if (x > a) {
+                b = a;
+                a = x;
+            } else if (x > b) {
+                b = x;
+            }
+        }
+        gs[g] = R.best == 2 ? a + b : a;
+    }
+    __syncwarp();
+    kept = 0;
+    for (int i = 0; i < R.G; i += LPT) {
+        const int g = i + sub;
+        bool keep = false;
+        if (g < R.G) {
+            const V mine = gs[g];
+            int rank = 0;
+            for (int o = 0; o < R.G; ++o) {
+                const V x = gs[o];
+                rank += (x > mine || (x == mine && o < g)) ? 1 : 0;
+            }
+            keep = rank < R.top_groups;
+            if (sizeof(V) == 4 && SCORES) {
+                // sums of two are off by up to twice as much; unsure: a kept group that could fall
+                // out, or a dropped one that could come in
+                const float t2 = 2.0f * tol * (1.0f + fabsf(static_cast<float>(mine)));
+                int above = 0, near = 0;
+                for (int o = 0; o < R.G; ++o) {
+                    const float d = static_cast<float>(gs[o]) - static_cast<float>(mine);
+                    above += d > t2 ? 1 : 0;
+                    near += (o != g && fabsf(d) <= t2) ? 1 : 0;
+                }
+                unsure |= near > 0 && above < R.top_groups && above + near >= R.top_groups;
+            }
+        }
+        const unsigned b = __ballot_sync(kFull, keep);
+        kept |= ((b >> (tok * LPT)) & kMine) << i;
+    }
+    return unsure;
+}
+
+// Bit j: the lane's expert e0 + j is in a group that stays.
+template <int VPL>
+__device__ __forceinline__ unsigned group_alive(unsigned kept, int e0, const Rule& R) {
+    unsigned alive = 0;
+    for (int g = e0 / R.S; g < R.G && g * R.S < e0 + VPL; ++g) {
+        if (!((kept >> g) & 1u)) continue;
+        const int lo = max(g * R.S - e0, 0), hi = min((g + 1) * R.S - e0, VPL);
+        alive |= ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+    }
+    return alive;
+}
+
 // Chooses the experts of the warp's tokens: slot[k] of each. V = float: returns whether a
 // choice lies too near a border to be certain (true for some lane of the token).
 // SCORES: some order needs the scores (a bias, or group sums).
@@ -186,59 +257,9 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
     // 17 + 21 units for 256 terms.
     const float tol = R.sigmoid ? 0x1p-20f : 0x1p-17f;
     if (R.G > 1) {
-        V* val = sm.val + tok * padded(LPT * VPL);
-        V* gs = sm.gscore + tok * R.G;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) val[pad_e(e0 + j)] = v[j];
-        __syncwarp();
-        for (int g = sub; g < R.G; g += LPT) {
-            V a = -INFINITY, b = -INFINITY;
-            for (int i = 0; i < R.S; ++i) {
-                const V x = val[pad_e(g * R.S + i)];
-                if (x > a) {
-                    b = a;
-                    a = x;
-                } else if (x > b) {
-                    b = x;
-                }
-            }
-            gs[g] = R.best == 2 ? a + b : a;
-        }
-        __syncwarp();
-        unsigned kept = 0;
-        for (int i = 0; i < R.G; i += LPT) {
-            const int g = i + sub;
-            bool keep = false;
-            if (g < R.G) {
-                const V mine = gs[g];
-                int rank = 0;
-                for (int o = 0; o < R.G; ++o) {
-                    const V x = gs[o];
-                    rank += (x > mine || (x == mine && o < g)) ? 1 : 0;
-                }
-                keep = rank < R.top_groups;
-                if (kFast && SCORES) {
-                    // sums of two are off by up to twice as much
-                    const float t2 = 2.0f * tol * (1.0f + fabsf(static_cast<float>(mine)));
-                    int above = 0, near = 0;
-                    for (int o = 0; o < R.G; ++o) {
-                        const float d = static_cast<float>(gs[o]) - static_cast<float>(mine);
-                        above += d > t2 ? 1 : 0;
-                        near += (o != g && fabsf(d) <= t2) ? 1 : 0;
-                    }
-                    // a kept group that could fall out, or a dropped one that could come in
-                    unsure |= near > 0 && above < R.top_groups && above + near >= R.top_groups;
-                }
-            }
-            const unsigned b = __ballot_sync(kFull, keep);
-            kept |= ((b >> g0) & kMine) << i;
-        }
-        unsigned alive = 0;
-        for (int g = e0 / R.S; g < R.G && g * R.S < e0 + VPL; ++g) {
-            if (!((kept >> g) & 1u)) continue;
-            const int lo = max(g * R.S - e0, 0), hi = min((g + 1) * R.S - e0, VPL);
-            alive |= ((1u << hi) - 1u) & ~((1u << lo) - 1u);
-        }
+        unsigned kept;
+        unsure = group_kept<V, LPT, VPL, SCORES>(v, e0, tok, R, sm.val, sm.gscore, tol, kept);
+        const unsigned alive = group_alive<VPL>(kept, e0, R);
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
             if (!((alive >> j) & 1u)) key[j] = 0;
@@ -282,44 +303,181 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
     return unsure;
 }
 
-// The same in fp64, out of line: it is rare and would cost the others registers.
-template <typename T, int LPT, int VPL>
-__device__ __noinline__ void choose_exactly(const T* row, bool vec, bool valid, const float* __restrict__ bias, Rule R,
-                                            int* slot, double* val) {
+// The same by rounds from the row itself, out of line: it is rare and would cost the
+// others registers. V = double: the exact choice.
+template <typename V, typename T, int LPT, int VPL, bool SCORES>
+__device__ __noinline__ void choose_again(const T* row, bool vec, bool valid, const float* __restrict__ bias, Rule R,
+                                          int* slot, float* slot_v, V* val) {
     float l[VPL];
     load_logits<T, VPL>(row, (threadIdx.x % LPT) * VPL, R.E, vec, valid, l);
-    WarpSmem<double> sm{slot, nullptr, val, val + (32 / LPT) * padded(LPT * VPL)};
-    choose<double, T, LPT, VPL, true>(l, row, bias, R, sm);
+    WarpSmem<V> sm{slot, slot_v, val, val + (32 / LPT) * padded(LPT * VPL)};
+    choose<V, T, LPT, VPL, SCORES>(l, row, bias, R, sm);
+}
+
+// A whole warp on one token (fp32). The largest value of each lane gives a threshold
+// that at least K (with the border test K + 1) values reach; the few that reach it are
+// collected, a lane each, and ranked by counting: about 160 instructions where rounds
+// take 450 (E = 256, K = 8). Returns false where more than 32 reach it (equal values).
+// Dropped experts are NaN, which no comparison lets through; masked ones -inf.
+template <typename T, int VPL, bool SCORES>
+__device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const T* row, const float* __restrict__ bias,
+                                                    const Rule& R, const WarpSmem<float>& sm, float2* cand, bool& unsure) {
+    const int lane = threadIdx.x & 31, e0 = lane * VPL;
+    const float nan = __int_as_float(0x7fffffff);
+    const float tol = R.sigmoid ? 0x1p-20f : 0x1p-17f;  // as in choose()
+    unsure = false;
+    float m = 0.0f, z = 1.0f;
+    if (SCORES && !R.sigmoid) softmax_stats<float, 32, VPL>(l, e0, R.E, m, z);
+    const float inv_z = 1.0f / z;
+    float v[VPL], order[VPL];  // what groups, what experts are compared by
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        const int e = e0 + j;
+        v[j] = l[j];
+        order[j] = l[j];
+        if (SCORES) {
+            v[j] = R.sigmoid ? sigmoid_v(l[j]) : expf(l[j] - m) * inv_z;
+            if (bias) {
+                if (e < R.E) v[j] += bias[e];
+                order[j] = v[j];
+            }
+        }
+        if (is_masked(l[j]) || order[j] != order[j]) v[j] = order[j] = -INFINITY;
+        if (e >= R.E) order[j] = nan;
+    }
+    if (R.G > 1) {
+        unsigned kept = 0;
+        const int L = R.S / VPL;  // lanes a group spans
+        if (R.S % VPL == 0 && (L & (L - 1)) == 0) {
+            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                b = fmaxf(b, fminf(a, v[j]));
+                a = fmaxf(a, v[j]);
+            }
+            for (int off = 1; off < L; off <<= 1) {
+                const float oa = __shfl_xor_sync(kFull, a, off), ob = __shfl_xor_sync(kFull, b, off);
+                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                a = fmaxf(a, oa);
+            }
+            const float mine = R.best == 2 ? a + b : a;
+            const int g = lane / L;
+            const float t2 = SCORES ? 2.0f * tol * (1.0f + fabsf(mine)) : 0.0f;
+            int rank = 0, above = 0, near = 0;
+            for (int o = 0; o < R.G; ++o) {
+                const float x = __shfl_sync(kFull, mine, o * L);
+                rank += (x > mine || (x == mine && o < g)) ? 1 : 0;
+                if (SCORES) {
+                    above += x - mine > t2 ? 1 : 0;
+                    near += (o != g && fabsf(x - mine) <= t2) ? 1 : 0;
+                }
+            }
+            const bool in = g < R.G;
+            if (SCORES) unsure = in && near > 0 && above < R.top_groups && above + near >= R.top_groups;
+            const bool keep = in && rank < R.top_groups;
+            if (!keep)
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) order[j] = nan;
+        } else {
+            unsure = group_kept<float, 32, VPL, SCORES>(v, e0, 0, R, sm.val, sm.gscore, tol, kept);
+            unsigned alive = group_alive<VPL>(kept, e0, R);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (!((alive >> j) & 1u)) order[j] = nan;
+        }
+    }
+    const bool check = SCORES && bias;
+    const int need = check ? R.K + 1 : R.K;
+    float top = nan;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) top = fmaxf(top, order[j]);
+    uint32_t cur = top != top ? 0u : key_of(top);
+    float tau = -INFINITY;
+    for (int reached = 0;;) {
+        const uint32_t mx = __reduce_max_sync(kFull, cur);
+        if (mx == 0) break;
+        const unsigned b = __ballot_sync(kFull, cur == mx);
+        reached += __popc(b);
+        if (reached >= need) {
+            tau = value_of(mx);
+            break;
+        }
+        if (cur == mx) cur = 0;
+    }
+    int total = 0;
+    const unsigned below = (1u << lane) - 1u;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        const bool in = order[j] >= tau;
+        const unsigned b = __ballot_sync(kFull, in);
+        const int at = total + __popc(b & below);
+        if (in && at < 32) cand[at] = make_float2(order[j], __int_as_float(e0 + j));
+        total += __popc(b);
+    }
+    if (total > 32) return false;
+    __syncwarp();
+    const float2 mine = lane < total ? cand[lane] : make_float2(nan, 0.0f);
+    const int my_e = __float_as_int(mine.y);
+    int rank = 0;
+    for (int o = 0; o < total; ++o) {
+        const float2 c = cand[o];
+        rank += (c.x > mine.x || (c.x == mine.x && __float_as_int(c.y) < my_e)) ? 1 : 0;
+    }
+    if (lane < total && rank < need) {
+        sm.slot[rank] = my_e;
+        sm.slot_v[rank] = mine.x;
+    }
+    if (lane == 0 && total < need) sm.slot[R.K] = -1;
+    __syncwarp();
+    if (check && lane < R.K) {
+        const int ea = sm.slot[lane], eb = sm.slot[lane + 1];
+        if (eb >= 0) {
+            const float a = sm.slot_v[lane], b = sm.slot_v[lane + 1];
+            if (a - b <= tol * (1.0f + fabsf(a)) && !(to_f(row[ea]) == to_f(row[eb]) && bias[ea] == bias[eb])) unsure = true;
+        }
+    }
+    return true;
 }
 
 // Bytes of one warp's area: slots, and (8-byte elements) group values and scores.
 __host__ __device__ inline int warp_bytes(const Rule& R, int lpt, int vpl) {
     const int tpw = 32 / lpt;
-    int b = (tpw * (R.K + 1) * 8 + 7) / 8 * 8;
+    int b = tpw * (R.K + 1) * 8 + (lpt == 32 ? 256 : 0);  // slots; a whole warp's candidates
     if (R.G > 1) b += tpw * (padded(lpt * vpl) + R.G) * 8;
     return b;
 }
 
-// Routes the warp's tokens t (one per lane group; valid: t < T): writes expert_idx and
+// Routes the warp's tokens t (one per lane group; valid: t < T) with logits l: writes expert_idx and
 // weights, adds to the block's histogram. s_idx: the pairs' experts kept for the
 // one-block kernel, or NULL.
 template <typename T, int LPT, int VPL, bool SCORES>
-__device__ __forceinline__ void route_tokens(const T* logits, int64_t ld, int64_t t, bool valid, bool vec,
+__device__ __forceinline__ void route_tokens(const float (&l)[VPL], const T* logits, int64_t ld, int64_t t, bool valid, bool vec,
                                              const float* __restrict__ bias, const Rule& R, uint8_t* area, int* hist,
                                              int32_t* __restrict__ expert_idx, float* __restrict__ weights, int* s_idx) {
     constexpr int TPW = 32 / LPT;
     const int lane = threadIdx.x & 31, sub = lane % LPT, tok = lane / LPT, e0 = sub * VPL;
     const T* row = logits + (valid ? t : 0) * ld;
-    float l[VPL];
-    load_logits<T, VPL>(row, e0, R.E, vec, valid, l);
     int* slots = reinterpret_cast<int*>(area);
-    double* wide = reinterpret_cast<double*>(area + (TPW * (R.K + 1) * 8 + 7) / 8 * 8);
+    float* slot_v = reinterpret_cast<float*>(slots + TPW * (R.K + 1));
+    float2* cand = reinterpret_cast<float2*>(area + TPW * (R.K + 1) * 8);
+    double* wide = reinterpret_cast<double*>(area + TPW * (R.K + 1) * 8 + (LPT == 32 ? 256 : 0));
     float* narrow = reinterpret_cast<float*>(wide);
-    WarpSmem<float> sm{slots, reinterpret_cast<float*>(slots + TPW * (R.K + 1)), narrow,
-                       narrow + TPW * padded(LPT * VPL)};
-    const bool unsure = choose<float, T, LPT, VPL, SCORES>(l, row, bias, R, sm);
-    if (SCORES && __any_sync(kFull, unsure && valid))
-        choose_exactly<T, LPT, VPL>(row, vec, valid, bias, R, slots, wide);
+    WarpSmem<float> sm{slots, slot_v, narrow, narrow + TPW * padded(LPT * VPL)};
+    bool unsure;
+    if constexpr (LPT == 32) {
+        const bool done = choose_by_threshold<T, VPL, SCORES>(l, row, bias, R, sm, cand, unsure);
+        if (!done) {
+            __syncwarp();
+            if (SCORES) unsure = true;
+            else choose_again<float, T, LPT, VPL, SCORES>(row, vec, valid, bias, R, slots, slot_v, narrow);
+        }
+    } else {
+        unsure = choose<float, T, LPT, VPL, SCORES>(l, row, bias, R, sm);
+    }
+    if (SCORES && __any_sync(kFull, unsure && valid)) {
+        __syncwarp();
+        choose_again<double, T, LPT, VPL, SCORES>(row, vec, valid, bias, R, slots, nullptr, wide);
+    }
     float m = 0.0f, z = 1.0f;
     if (!R.sigmoid && !R.renorm) softmax_stats<float, LPT, VPL>(l, e0, R.E, m, z);
     const int* slot = slots + tok * (R.K + 1);
@@ -417,7 +575,7 @@ __device__ __forceinline__ void scatter_pairs(const int* idx, int n, int32_t p0,
 // ---------------------------------------------------------------- kernels
 // Tokens [b * tpb, (b + 1) * tpb) of block b; blk_counts [gridDim.x][E].
 template <typename T, int LPT, int VPL, bool SCORES>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 topk_route_kernel(const T* __restrict__ logits, int64_t ld, int64_t T_, int tpb, bool vec,
                   const float* __restrict__ bias, Rule R, int32_t* __restrict__ expert_idx,
                   float* __restrict__ weights, int32_t* __restrict__ blk_counts) {
@@ -431,9 +589,18 @@ topk_route_kernel(const T* __restrict__ logits, int64_t ld, int64_t T_, int tpb,
     __syncthreads();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpb;
     const int64_t t1 = t0 + tpb < T_ ? t0 + tpb : T_;
-    for (int64_t t = t0 + warp * TPW; t < t1; t += kWarps * TPW)
-        route_tokens<T, LPT, VPL, SCORES>(logits, ld, t + tok, t + tok < t1, vec, bias, R, area, hist, expert_idx,
-                                          weights, nullptr);
+    const int e0 = ((threadIdx.x & 31) % LPT) * VPL;
+    float next[VPL];
+    int64_t t = t0 + warp * TPW + tok;
+    load_logits<T, VPL>(logits + (t < t1 ? t : 0) * ld, e0, R.E, vec, t < t1, next);
+    for (; t - tok < t1; t += kWarps * TPW) {
+        float l[VPL];
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) l[j] = next[j];
+        const int64_t tn = t + kWarps * TPW;
+        load_logits<T, VPL>(logits + (tn < t1 ? tn : 0) * ld, e0, R.E, vec, tn < t1, next);
+        route_tokens<T, LPT, VPL, SCORES>(l, logits, ld, t, t < t1, vec, bias, R, area, hist, expert_idx, weights, nullptr);
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < R.E; e += kThreads) blk_counts[static_cast<int64_t>(blockIdx.x) * R.E + e] = hist[e];
 }
@@ -455,9 +622,12 @@ topk_route_small_kernel(const T* __restrict__ logits, int64_t ld, int T_, bool v
     const int warp = threadIdx.x >> 5, tok = (threadIdx.x & 31) / LPT;
     for (int e = threadIdx.x; e < R.E; e += kSmallThreads) hist[e] = 0;
     __syncthreads();
-    for (int t = warp * TPW; t < T_; t += WARPS * TPW)
-        route_tokens<T, LPT, VPL, SCORES>(logits, ld, t + tok, t + tok < T_, vec, bias, R,
-                                          areas + warp * warp_bytes(R, LPT, VPL), hist, expert_idx, weights, s_idx);
+    for (int t = warp * TPW + tok; t - tok < T_; t += WARPS * TPW) {
+        float l[VPL];
+        load_logits<T, VPL>(logits + static_cast<int64_t>(t < T_ ? t : 0) * ld, ((threadIdx.x & 31) % LPT) * VPL, R.E, vec, t < T_, l);
+        route_tokens<T, LPT, VPL, SCORES>(l, logits, ld, t, t < T_, vec, bias, R, areas + warp * warp_bytes(R, LPT, VPL),
+                                          hist, expert_idx, weights, s_idx);
+    }
     __syncthreads();
     const int e = threadIdx.x;
     const int c = e < R.E ? hist[e] : 0;
@@ -651,28 +821,29 @@ struct RouteArgs {
     int32_t* blk_base;
 };
 
-// Tokens one block of 32 warps handles in at most two steps take the one-block kernel, if
-// its shared memory holds them. Returns the bytes, 0 if not.
-int small_smem(const RouteArgs& a, int ep, int warp_area) {
-    constexpr int kLimit = 200 * 1024;
-    if (a.T * ep > 2 * 32 * 512 || a.T * a.R.K > kSmallPairs) return 0;
+// Shared memory of the one-block kernel, 0 where there are too many tokens for it: at most
+// four a warp.
+int small_smem(const RouteArgs& a, int warp_area) {
+    if (a.T > 4 * (kSmallThreads / 32) || a.T * a.R.K > kSmallPairs) return 0;
     const int per_warp = warp_area > a.R.E * 4 ? warp_area : a.R.E * 4;
     const int smem = kMaxE * 4 + (static_cast<int>(a.T) * a.R.K + 3) / 4 * 16 + kSmallThreads / 32 * per_warp;
-    return smem <= kLimit ? smem : 0;
+    return smem <= 200 * 1024 ? smem : 0;
+}
+
+template <typename T, int VPL, bool SCORES>
+cudaError_t route_small(const RouteArgs& a, int smem, cudaStream_t s) {
+    auto kernel = topk_route_small_kernel<T, 32, VPL, SCORES>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(1), dim3(kSmallThreads), smem, s, static_cast<const T*>(a.logits), a.ld,
+                      static_cast<int>(a.T), a.vec, a.bias, a.R, a.out.expert_idx, a.weights, a.out.counts, a.out.offsets,
+                      a.out.perm);
 }
 
 template <typename T, int LPT, int VPL, bool SCORES>
 cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
     const Rule& R = a.R;
     const int wb = warp_bytes(R, LPT, VPL);
-    if (const int smem = small_smem(a, LPT * VPL, wb)) {
-        auto kernel = topk_route_small_kernel<T, LPT, VPL, SCORES>;
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-        if (e != cudaSuccess) return e;
-        return launch_pdl(kernel, dim3(1), dim3(kSmallThreads), smem, s, static_cast<const T*>(a.logits), a.ld,
-                          static_cast<int>(a.T), a.vec, a.bias, R, a.out.expert_idx, a.weights, a.out.counts,
-                          a.out.offsets, a.out.perm);
-    }
     int sms = 0;
     cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess) return e;
@@ -698,15 +869,22 @@ cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
                       a.T * R.K, tpb * R.K, R.E, a.blk_base, a.out.counts, a.out.offsets, a.out.perm);
 }
 
+// Few tokens: one block, a warp per token (the shortest chain). Many: a token per 1 to 8
+// lanes up to 64 experts, where a warp's rounds serve several tokens, a warp per token above.
 template <typename T, bool SCORES>
 cudaError_t route_width(const RouteArgs& a, cudaStream_t s) {
-    const int E = a.R.E;
+    const int E = a.R.E, vpl = E <= 64 ? 2 : E <= 128 ? 4 : 8;
+    if (const int smem = small_smem(a, warp_bytes(a.R, 32, vpl))) {
+        if (vpl == 2) return route_small<T, 2, SCORES>(a, smem, s);
+        if (vpl == 4) return route_small<T, 4, SCORES>(a, smem, s);
+        return route_small<T, 8, SCORES>(a, smem, s);
+    }
     if (E <= 8) return route_launch<T, 1, 8, SCORES>(a, s);
-    if (E <= 16) return route_launch<T, 1, 16, SCORES>(a, s);
-    if (E <= 32) return route_launch<T, 2, 16, SCORES>(a, s);
-    if (E <= 64) return route_launch<T, 4, 16, SCORES>(a, s);
-    if (E <= 128) return route_launch<T, 8, 16, SCORES>(a, s);
-    return route_launch<T, 16, 16, SCORES>(a, s);
+    if (E <= 16) return route_launch<T, 2, 8, SCORES>(a, s);
+    if (E <= 32) return route_launch<T, 4, 8, SCORES>(a, s);
+    if (E <= 64) return route_launch<T, 8, 8, SCORES>(a, s);
+    if (E <= 128) return route_launch<T, 32, 4, SCORES>(a, s);
+    return route_launch<T, 32, 8, SCORES>(a, s);
 }
 
 template <typename T>
