@@ -11,7 +11,7 @@
 // Choices are exact. Without a bias the order of v is that of the logits, which are
 // compared as they are. With a bias (or sums of scores per group) v is computed in
 // fp32, and where two neighbours in the result lie within the error of that
-// computation the warp repeats the choice in fp64; about 1 % of the warps do.
+// computation the token is chosen again in fp64; about one in a thousand is.
 //
 // A token belongs to LPT lanes with VPL consecutive experts each. Up to 64 experts a
 // warp works on 32 / LPT tokens at once: K rounds of a local maximum, a shuffle maximum
@@ -22,6 +22,7 @@
 // route.cu). Few tokens take one launch of one block that does all three.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "checks.h"
 #include "common.cuh"
@@ -39,6 +40,9 @@ constexpr int kSmallThreads = 1024;
 constexpr int kMaxBlocks = 1024;      // rows of per-block counts the workspace holds
 constexpr int kSmallPairs = 8192;     // pairs the one-block kernel keeps in shared memory
 constexpr unsigned kFull = 0xffffffffu;
+
+// What the choice compares: logits, or scores (a bias, or group sums, make the difference).
+enum Mode : int { kLogits = 0, kSigmoid = 1, kSoftmax = 2 };
 
 struct Rule {
     int E, K, G, S, top_groups, best;  // S: experts per group
@@ -74,9 +78,15 @@ struct KeyOf<double> {
 __device__ __forceinline__ float exp_v(float x) { return expf(x); }
 __device__ __forceinline__ double exp_v(double x) { return exp(x); }
 // Only compared (fp32): an absolute error of 7 * 2^-24 is inside the border test. The
-// fast exponential is off by 2 + 1.173 |l| units in the last place at most, which times
-// s (1 - s) stays below 1.3 * 2^-24; the sum adds 1 and the division 4.
-__device__ __forceinline__ float sigmoid_v(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
+// exponent l log2 e is rounded once (|l| 2^-23 relative in the power, at most 1.3 * 2^-24
+// after the factor s (1 - s)), ex2 and rcp are off by 2 units in the last place at most
+// each, the sums by one.
+__device__ __forceinline__ float sigmoid_v(float l) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 __device__ __forceinline__ double sigmoid_v(double l) { return 1.0 / (1.0 + exp(-l)); }
 
 template <int LPT, typename V>
@@ -115,6 +125,12 @@ __device__ __forceinline__ void load_logits(const T* row, int e0, int E, bool ve
     }
 }
 
+template <int VPL>
+__device__ __forceinline__ void load_bias(const float* bias, int e0, int E, float (&b)[VPL]) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) b[j] = bias && e0 + j < E ? bias[e0 + j] : 0.0f;
+}
+
 __device__ __forceinline__ bool is_masked(float l) { return !(l > -INFINITY); }
 
 // Maximum and sum of exponentials of a softmax row over its lanes (fp32 or fp64). A row
@@ -151,7 +167,7 @@ __host__ __device__ constexpr int padded(int ep) { return ep + ep / 32 + 1; }
 
 // The groups that stay, through shared memory: bit g of kept. Returns whether fp32 leaves
 // that open.
-template <typename V, int LPT, int VPL, bool SCORES>
+template <typename V, int LPT, int VPL, int MODE>
 __device__ __forceinline__ bool group_kept(const V (&v)[VPL], int e0, int tok, const Rule& R, V* vals, V* gscores, float tol,
                                            unsigned& kept) {
     constexpr unsigned kMine = LPT == 32 ? kFull : (1u << (LPT & 31)) - 1u;
@@ -188,7 +204,7 @@ __device__ __forceinline__ bool group_kept(const V (&v)[VPL], int e0, int tok, c
                 rank += (x > mine || (x == mine && o < g)) ? 1 : 0;
             }
             keep = rank < R.top_groups;
-            if (sizeof(V) == 4 && SCORES) {
+            if (sizeof(V) == 4 && MODE != kLogits) {
                 // sums of two are off by up to twice as much; unsure: a kept group that could fall
                 // out, or a dropped one that could come in
                 const float t2 = 2.0f * tol * (1.0f + fabsf(static_cast<float>(mine)));
@@ -221,8 +237,7 @@ __device__ __forceinline__ unsigned group_alive(unsigned kept, int e0, const Rul
 
 // Chooses the experts of the warp's tokens: slot[k] of each. V = float: returns whether a
 // choice lies too near a border to be certain (true for some lane of the token).
-// SCORES: some order needs the scores (a bias, or group sums).
-template <typename V, typename T, int LPT, int VPL, bool SCORES>
+template <typename V, typename T, int LPT, int VPL, int MODE>
 __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, const float* __restrict__ bias,
                                        const Rule& R, const WarpSmem<V>& sm) {
     using Key = typename KeyOf<V>::type;
@@ -230,10 +245,10 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
     const int lane = threadIdx.x & 31, sub = lane % LPT, tok = lane / LPT, g0 = tok * LPT, e0 = sub * VPL;
     constexpr unsigned kMine = LPT == 32 ? kFull : (1u << (LPT & 31)) - 1u;
     V m = 0, z = 1;
-    if (SCORES && !R.sigmoid) softmax_stats<V, LPT, VPL>(l, e0, R.E, m, z);
+    if (MODE == kSoftmax) softmax_stats<V, LPT, VPL>(l, e0, R.E, m, z);
     const V inv_z = V(1) / z;
     auto score = [&](float x) -> V {
-        return R.sigmoid ? sigmoid_v(static_cast<V>(x)) : exp_v(static_cast<V>(x) - m) * inv_z;
+        return MODE == kSigmoid ? sigmoid_v(static_cast<V>(x)) : exp_v(static_cast<V>(x) - m) * inv_z;
     };
     Key key[VPL];
     V v[VPL];  // what groups are scored by
@@ -241,7 +256,7 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
     for (int j = 0; j < VPL; ++j) {
         const int e = e0 + j;
         V order;
-        if (SCORES) {
+        if (MODE != kLogits) {
             v[j] = score(l[j]);
             if (bias && e < R.E) v[j] += static_cast<V>(bias[e]);
             order = bias ? v[j] : static_cast<V>(l[j]);
@@ -255,16 +270,16 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
     bool unsure = false;
     // border of two values in fp32; see sigmoid_v. The softmax adds the error of its sum:
     // 17 + 21 units for 256 terms.
-    const float tol = R.sigmoid ? 0x1p-20f : 0x1p-17f;
+    const float tol = MODE == kSigmoid ? 0x1p-20f : 0x1p-17f;
     if (R.G > 1) {
         unsigned kept;
-        unsure = group_kept<V, LPT, VPL, SCORES>(v, e0, tok, R, sm.val, sm.gscore, tol, kept);
+        unsure = group_kept<V, LPT, VPL, MODE>(v, e0, tok, R, sm.val, sm.gscore, tol, kept);
         const unsigned alive = group_alive<VPL>(kept, e0, R);
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
             if (!((alive >> j) & 1u)) key[j] = 0;
     }
-    constexpr bool kCheck = kFast && SCORES;
+    constexpr bool kCheck = kFast && MODE != kLogits;
     int* slot = sm.slot + tok * (R.K + 1);
     float* slot_v = sm.slot_v + tok * (R.K + 1);
     const int rounds = (kCheck && bias) ? R.K + 1 : R.K;
@@ -303,216 +318,362 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
     return unsure;
 }
 
-// The same by rounds from the row itself, out of line: it is rare and would cost the
-// others registers. V = double: the exact choice.
-template <typename V, typename T, int LPT, int VPL, bool SCORES>
-__device__ __noinline__ void choose_again(const T* row, bool vec, bool valid, const float* __restrict__ bias, Rule R,
-                                          int* slot, float* slot_v, V* val) {
-    float l[VPL];
-    load_logits<T, VPL>(row, (threadIdx.x % LPT) * VPL, R.E, vec, valid, l);
-    WarpSmem<V> sm{slot, slot_v, val, val + (32 / LPT) * padded(LPT * VPL)};
-    choose<V, T, LPT, VPL, SCORES>(l, row, bias, R, sm);
-}
-
-// A whole warp on one token (fp32). The largest value of each lane gives a threshold
-// that at least K (with the border test K + 1) values reach; the few that reach it are
-// collected, a lane each, and ranked by counting: about 160 instructions where rounds
-// take 450 (E = 256, K = 8). Returns false where more than 32 reach it (equal values).
+// A whole warp on one token (fp32). A threshold that at least K (with the border test
+// K + 1) values reach gives a few candidates, a lane each, which are ranked by counting.
+// The threshold is the last token's, where that leaves between K + 1 and 32 candidates,
+// else the largest of the lanes' maxima that enough lanes reach. Returns false where the
+// fp32 values leave the choice open, or more than 32 reach the threshold (equal values).
 // Dropped experts are NaN, which no comparison lets through; masked ones -inf.
-template <typename T, int VPL, bool SCORES>
-__device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const T* row, const float* __restrict__ bias,
-                                                    const Rule& R, const WarpSmem<float>& sm, float2* cand, bool& unsure) {
+template <typename T, int VPL, int MODE>
+__device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const float (&b)[VPL], const T* row,
+                                                    const float* __restrict__ bias, const Rule& R, int* slot,
+                                                    float* slot_v, float2* cand, int* found, float* groups, float2& stats,
+                                                    float& guess) {
     const int lane = threadIdx.x & 31, e0 = lane * VPL;
     const float nan = __int_as_float(0x7fffffff);
-    const float tol = R.sigmoid ? 0x1p-20f : 0x1p-17f;  // as in choose()
-    unsure = false;
-    float m = 0.0f, z = 1.0f;
-    if (SCORES && !R.sigmoid) softmax_stats<float, 32, VPL>(l, e0, R.E, m, z);
-    const float inv_z = 1.0f / z;
-    float v[VPL], order[VPL];  // what groups, what experts are compared by
+    constexpr float tol = MODE == kSigmoid ? 0x1p-20f : 0x1p-17f;  // as in choose()
+    bool unsure = false;
+    float order[VPL];
+    if (MODE == kSoftmax || (!R.sigmoid && !R.renorm)) softmax_stats<float, 32, VPL>(l, e0, R.E, stats.x, stats.y);
+    if (MODE == kLogits) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-        const int e = e0 + j;
-        v[j] = l[j];
-        order[j] = l[j];
-        if (SCORES) {
-            v[j] = R.sigmoid ? sigmoid_v(l[j]) : expf(l[j] - m) * inv_z;
-            if (bias) {
-                if (e < R.E) v[j] += bias[e];
-                order[j] = v[j];
-            }
+        for (int j = 0; j < VPL; ++j) order[j] = is_masked(l[j]) ? -INFINITY : l[j];
+    } else {
+        const float inv_z = MODE == kSoftmax ? 1.0f / stats.y : 1.0f;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const float s = (MODE == kSigmoid ? sigmoid_v(l[j]) : expf(l[j] - stats.x) * inv_z) + b[j];
+            order[j] = l[j] > -INFINITY && (MODE == kSigmoid || s == s) ? s : -INFINITY;
         }
-        if (is_masked(l[j]) || order[j] != order[j]) v[j] = order[j] = -INFINITY;
-        if (e >= R.E) order[j] = nan;
     }
+    bool keep = true;
+    unsigned alive = 0xffffffffu;
     if (R.G > 1) {
-        unsigned kept = 0;
         const int L = R.S / VPL;  // lanes a group spans
         if (R.S % VPL == 0 && (L & (L - 1)) == 0) {
-            float a = -INFINITY, b = -INFINITY;
+            float a = -INFINITY, c = -INFINITY;
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
-                b = fmaxf(b, fminf(a, v[j]));
-                a = fmaxf(a, v[j]);
+                c = fmaxf(c, fminf(a, order[j]));
+                a = fmaxf(a, order[j]);
             }
             for (int off = 1; off < L; off <<= 1) {
-                const float oa = __shfl_xor_sync(kFull, a, off), ob = __shfl_xor_sync(kFull, b, off);
-                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                const float oa = __shfl_xor_sync(kFull, a, off), oc = __shfl_xor_sync(kFull, c, off);
+                c = fmaxf(fminf(a, oa), fmaxf(c, oc));
                 a = fmaxf(a, oa);
             }
-            const float mine = R.best == 2 ? a + b : a;
-            const int g = lane / L;
-            const float t2 = SCORES ? 2.0f * tol * (1.0f + fabsf(mine)) : 0.0f;
-            int rank = 0, above = 0, near = 0;
-            for (int o = 0; o < R.G; ++o) {
-                const float x = __shfl_sync(kFull, mine, o * L);
-                rank += (x > mine || (x == mine && o < g)) ? 1 : 0;
-                if (SCORES) {
-                    above += x - mine > t2 ? 1 : 0;
-                    near += (o != g && fabsf(x - mine) <= t2) ? 1 : 0;
+            const float mine = R.best == 2 ? a + c : a;
+            const int g = lane >> (31 - __clz(L));
+            // the group's lanes compare it with the others in turn: counts of groups above, and (scores)
+            // of groups too near to tell, itself among them. Sums of two are off by up to twice as much.
+            const float t2 = MODE == kLogits || !(mine > -INFINITY) ? 0.0f : 2.0f * tol * (1.0f + fabsf(mine));
+            int count = 0;
+            for (int o0 = 0; o0 < R.G; o0 += L) {  // every lane takes the same number of turns
+                const int o = o0 + (lane & (L - 1));
+                const float x = __shfl_sync(kFull, mine, (o * L) & 31);
+                if (o < R.G) {
+                    if (MODE == kLogits) {
+                        count += (x > mine || (x == mine && o < g)) ? 1 : 0;
+                    } else {
+                        const float d = x - mine;
+                        count += d > t2 ? 1 : !(fabsf(d) > t2) ? 256 : 0;  // -inf - -inf counts as near
+                    }
                 }
             }
-            const bool in = g < R.G;
-            if (SCORES) unsure = in && near > 0 && above < R.top_groups && above + near >= R.top_groups;
-            const bool keep = in && rank < R.top_groups;
-            if (!keep)
-#pragma unroll
-                for (int j = 0; j < VPL; ++j) order[j] = nan;
+            for (int off = 1; off < L; off <<= 1) count += __shfl_xor_sync(kFull, count, off);
+            const int above = count & 255;
+            keep = g < R.G && above < R.top_groups;
+            if (MODE != kLogits) unsure = keep && above + (count >> 8) > R.top_groups;
         } else {
-            unsure = group_kept<float, 32, VPL, SCORES>(v, e0, 0, R, sm.val, sm.gscore, tol, kept);
-            unsigned alive = group_alive<VPL>(kept, e0, R);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (!((alive >> j) & 1u)) order[j] = nan;
+            unsigned kept;
+            unsure = group_kept<float, 32, VPL, MODE>(order, e0, 0, R, groups, groups + padded(32 * VPL), tol, kept);
+            alive = group_alive<VPL>(kept, e0, R);
         }
     }
-    const bool check = SCORES && bias;
+    const bool check = MODE != kLogits && bias;
+    if (MODE != kLogits && !bias) {  // groups were chosen by scores, experts are by logits
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) order[j] = is_masked(l[j]) ? -INFINITY : l[j];
+    }
+    const int mine_n = keep ? R.E - e0 : 0;  // experts of this lane that count
     const int need = check ? R.K + 1 : R.K;
-    float top = nan;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) top = fmaxf(top, order[j]);
-    uint32_t cur = top != top ? 0u : key_of(top);
-    float tau = -INFINITY;
-    for (int reached = 0;;) {
-        const uint32_t mx = __reduce_max_sync(kFull, cur);
-        if (mx == 0) break;
-        const unsigned b = __ballot_sync(kFull, cur == mx);
-        reached += __popc(b);
-        if (reached >= need) {
-            tau = value_of(mx);
-            break;
-        }
-        if (cur == mx) cur = 0;
-    }
-    int total = 0;
-    const unsigned below = (1u << lane) - 1u;
+    int n = 0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-        const bool in = order[j] >= tau;
-        const unsigned b = __ballot_sync(kFull, in);
-        const int at = total + __popc(b & below);
-        if (in && at < 32) cand[at] = make_float2(order[j], __int_as_float(e0 + j));
-        total += __popc(b);
+        if (j >= mine_n || !((alive >> j) & 1u)) order[j] = nan;
+        n += order[j] >= guess ? 1 : 0;
     }
-    if (total > 32) return false;
+    float tau = guess;
+    int total = __reduce_add_sync(kFull, n);
+    if (total < need || total > 32) {
+        float top = nan;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) top = fmaxf(top, order[j]);
+        uint32_t cur = top != top ? 0u : key_of(top);
+        tau = -INFINITY;
+        for (int reached = 0;;) {
+            const uint32_t mx = __reduce_max_sync(kFull, cur);
+            if (mx == 0) break;
+            const bool at_top = cur == mx;
+            reached += __popc(__ballot_sync(kFull, at_top));
+            if (reached >= need) {
+                tau = value_of(mx);
+                break;
+            }
+            if (at_top) cur = 0;
+        }
+        n = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) n += order[j] >= tau ? 1 : 0;
+        total = __reduce_add_sync(kFull, n);
+        if (total > 32) return false;
+    }
+    // the list's order does not matter: its entries are ranked by value and index
+    if (n) {
+        int at = atomicAdd(found, n);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (order[j] >= tau) cand[at++] = make_float2(order[j], __int_as_float(e0 + j));
+    }
     __syncwarp();
+    if (lane == 0) *found = 0;
     const float2 mine = lane < total ? cand[lane] : make_float2(nan, 0.0f);
     const int my_e = __float_as_int(mine.y);
     int rank = 0;
+#pragma unroll 4
     for (int o = 0; o < total; ++o) {
         const float2 c = cand[o];
         rank += (c.x > mine.x || (c.x == mine.x && __float_as_int(c.y) < my_e)) ? 1 : 0;
     }
-    if (lane < total && rank < need) {
-        sm.slot[rank] = my_e;
-        sm.slot_v[rank] = mine.x;
+    const bool in = lane < total && rank < need;
+    if (in) {
+        slot[rank] = my_e;
+        slot_v[rank] = mine.x;
     }
-    if (lane == 0 && total < need) sm.slot[R.K] = -1;
-    __syncwarp();
-    if (check && lane < R.K) {
-        const int ea = sm.slot[lane], eb = sm.slot[lane + 1];
-        if (eb >= 0) {
-            const float a = sm.slot_v[lane], b = sm.slot_v[lane + 1];
-            if (a - b <= tol * (1.0f + fabsf(a)) && !(to_f(row[ea]) == to_f(row[eb]) && bias[ea] == bias[eb])) unsure = true;
+    // the next token's guess: the value a few places behind the last one needed
+    const unsigned b_guess = __ballot_sync(kFull, lane < total && rank == min(total - 1, need + 4));
+    guess = __shfl_sync(kFull, mine.x, __ffs(b_guess) - 1);
+    if (check) {
+        __syncwarp();
+        if (lane < R.K && lane + 1 < total) {
+            const float x = slot_v[lane], y = slot_v[lane + 1];
+            if (x - y <= tol * (1.0f + fabsf(x))) {
+                // equal logits and equal biases are a true tie, in index order already
+                const int ea = slot[lane], eb = slot[lane + 1];
+                if (!(to_f(row[ea]) == to_f(row[eb]) && bias[ea] == bias[eb])) unsure = true;
+            }
         }
     }
-    return true;
+    return !__any_sync(kFull, unsure);
 }
 
-// Bytes of one warp's area: slots, and (8-byte elements) group values and scores.
+// Weight of a chosen expert with logit x. Each of `lanes` neighbouring lanes has one (on)
+// or none; stats: maximum and sum of the softmax row, where that is what divides.
+template <int LANES>
+__device__ __forceinline__ float weight_of(float x, bool on, float2 stats, const Rule& R) {
+    float m = 0.0f, z = 1.0f;
+    const float low = R.sigmoid ? (x >= 0.0f ? 0.0f : x) : x;  // keeps a NaN
+    if (R.renorm) {  // ratios: the largest chosen exponent is 0
+        m = on ? low : -INFINITY;
+#pragma unroll
+        for (int off = LANES / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+        if (m == -INFINITY) m = 0.0f;
+    } else if (!R.sigmoid) {
+        m = stats.x;
+        z = stats.y;
+    }
+    float p = expf(low - m);
+    if (R.sigmoid) p = p / (1.0f + expf(-fabsf(x)));
+    if (R.renorm) {
+        z = on ? p : 0.0f;
+#pragma unroll
+        for (int off = LANES / 2; off >= 1; off >>= 1) z += __shfl_xor_sync(kFull, z, off);
+        if (z == 0.0f) z = 1.0f;
+    }
+    return R.scale * (p / z);
+}
+
+// One token that the fp32 pass left open, by a whole warp: the choice by rounds (in fp64
+// where scores decide), weights and counts. Out of line: it is rare.
+template <typename T, int VPL, int MODE>
+__device__ __noinline__ void route_again(const T* row, int64_t t, bool vec, const float* __restrict__ bias, const Rule& R,
+                                         int* slot, float* slot_v, double* groups, int* hist,
+                                         int32_t* __restrict__ expert_idx, float* __restrict__ weights, int* s_idx) {
+    using V = typename std::conditional<MODE == kLogits, float, double>::type;
+    const int lane = threadIdx.x & 31, e0 = lane * VPL;
+    float l[VPL];
+    load_logits<T, VPL>(row, e0, R.E, vec, true, l);
+    V* val = reinterpret_cast<V*>(groups);
+    WarpSmem<V> sm{slot, slot_v, val, val + padded(32 * VPL)};
+    choose<V, T, 32, VPL, MODE>(l, row, bias, R, sm);
+    float2 stats = make_float2(0.0f, 1.0f);
+    if (!R.sigmoid && !R.renorm) softmax_stats<float, 32, VPL>(l, e0, R.E, stats.x, stats.y);
+    const bool on = lane < R.K;
+    const int e = on ? slot[lane] : 0;
+    const float w = weight_of<32>(on ? to_f(row[e]) : 0.0f, on, stats, R);
+    if (on) {
+        expert_idx[t * R.K + lane] = e;
+        weights[t * R.K + lane] = w;
+        atomicAdd(&hist[e], 1);
+        if (s_idx) s_idx[t * R.K + lane] = e;
+    }
+    __syncwarp();
+}
+
+// Shared memory of one warp: slots of its tokens (K + 1 experts and values each), softmax
+// statistics, candidates and their number, and with groups (8-byte elements, enough for
+// route_again) values and group scores.
+struct WarpArea {
+    int* slot;
+    float* slot_v;
+    float2* stats;
+    float2* cand;
+    int* found;  // zero between tokens
+    double* groups;
+};
+// Tokens whose slots a warp keeps: those it works on at once, or (a token per warp) those
+// whose weights it computes together, a lane per chosen expert.
+__host__ __device__ inline int slot_tokens(int lpt, int K) { return lpt < 32 ? 32 / lpt : K <= 4 ? 8 : K <= 8 ? 4 : 2; }
 __host__ __device__ inline int warp_bytes(const Rule& R, int lpt, int vpl) {
-    const int tpw = 32 / lpt;
-    int b = tpw * (R.K + 1) * 8 + (lpt == 32 ? 256 : 0);  // slots; a whole warp's candidates
-    if (R.G > 1) b += tpw * (padded(lpt * vpl) + R.G) * 8;
+    const int n = slot_tokens(lpt, R.K), tpw = 32 / lpt;
+    int b = n * (R.K + 1) * 8 + n * 8 + 256 + 8;
+    if (R.G > 1) {
+        const int again = padded(lpt < 32 ? 64 : 32 * vpl) + R.G, now = (tpw * (padded(lpt * vpl) + R.G) + 1) / 2;
+        b += 8 * (again > now ? again : now);
+    }
     return b;
 }
+__device__ __forceinline__ WarpArea warp_area(uint8_t* p, int lpt, int K) {
+    const int n = slot_tokens(lpt, K);
+    WarpArea a;
+    a.slot = reinterpret_cast<int*>(p);
+    a.slot_v = reinterpret_cast<float*>(p + n * (K + 1) * 4);
+    a.stats = reinterpret_cast<float2*>(p + n * (K + 1) * 8);
+    a.cand = a.stats + n;
+    a.found = reinterpret_cast<int*>(a.cand + 32);
+    a.groups = reinterpret_cast<double*>(a.found + 2);
+    return a;
+}
 
-// Routes the warp's tokens t (one per lane group; valid: t < T) with logits l: writes expert_idx and
-// weights, adds to the block's histogram. s_idx: the pairs' experts kept for the
-// one-block kernel, or NULL.
-template <typename T, int LPT, int VPL, bool SCORES>
-__device__ __forceinline__ void route_tokens(const float (&l)[VPL], const T* logits, int64_t ld, int64_t t, bool valid, bool vec,
-                                             const float* __restrict__ bias, const Rule& R, uint8_t* area, int* hist,
+// Routes tokens t0, t0 + step, ... below t1 (a token per group of LPT lanes: t0 is the
+// group's first): writes expert_idx and weights, adds to the block's histogram. s_idx:
+// the pairs' experts kept for the one-block kernel, or NULL.
+template <typename T, int LPT, int VPL, int MODE>
+__device__ __forceinline__ void route_tokens(const T* logits, int64_t ld, int64_t t0, int64_t t1, int64_t step, bool vec,
+                                             const float* __restrict__ bias, const Rule& R, const WarpArea& A, int* hist,
                                              int32_t* __restrict__ expert_idx, float* __restrict__ weights, int* s_idx) {
-    constexpr int TPW = 32 / LPT;
-    const int lane = threadIdx.x & 31, sub = lane % LPT, tok = lane / LPT, e0 = sub * VPL;
-    const T* row = logits + (valid ? t : 0) * ld;
-    int* slots = reinterpret_cast<int*>(area);
-    float* slot_v = reinterpret_cast<float*>(slots + TPW * (R.K + 1));
-    float2* cand = reinterpret_cast<float2*>(area + TPW * (R.K + 1) * 8);
-    double* wide = reinterpret_cast<double*>(area + TPW * (R.K + 1) * 8 + (LPT == 32 ? 256 : 0));
-    float* narrow = reinterpret_cast<float*>(wide);
-    WarpSmem<float> sm{slots, slot_v, narrow, narrow + TPW * padded(LPT * VPL)};
-    bool unsure;
+    const int lane = threadIdx.x & 31, sub = lane % LPT, tok = lane / LPT, e0 = sub * VPL, K = R.K;
+    const int64_t first = t0 - tok;  // the warp's first token
+    float next[VPL];
+    load_logits<T, VPL>(logits + (t0 < t1 ? t0 : 0) * ld, e0, R.E, vec, t0 < t1, next);
     if constexpr (LPT == 32) {
-        const bool done = choose_by_threshold<T, VPL, SCORES>(l, row, bias, R, sm, cand, unsure);
-        if (!done) {
+        const int batch = slot_tokens(32, K), lanes = 32 / batch;
+        float b[VPL];
+        load_bias<VPL>(bias, e0, R.E, b);
+        float guess = __int_as_float(0x7fffffff);
+        if (lane == 0) *A.found = 0;
+        __syncwarp();
+        for (int64_t tb = t0; tb < t1; tb += batch * step) {
+            unsigned open = 0;  // tokens of the batch left open
+            for (int i = 0; i < batch; ++i) {
+                const int64_t t = tb + i * step;
+                if (t >= t1) break;
+                float l[VPL];
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) l[j] = next[j];
+                const int64_t tn = t + step;
+                load_logits<T, VPL>(logits + (tn < t1 ? tn : 0) * ld, e0, R.E, vec, tn < t1, next);
+                float2 stats = make_float2(0.0f, 1.0f);
+                if (!choose_by_threshold<T, VPL, MODE>(l, b, logits + t * ld, bias, R, A.slot + i * (K + 1),
+                                                       A.slot_v + i * (K + 1), A.cand, A.found,
+                                                       reinterpret_cast<float*>(A.groups), stats, guess))
+                    open |= 1u << i;
+                if (lane == 0) A.stats[i] = stats;
+            }
             __syncwarp();
-            if (SCORES) unsure = true;
-            else choose_again<float, T, LPT, VPL, SCORES>(row, vec, valid, bias, R, slots, slot_v, narrow);
+            // weights of the batch: lane (i, k)
+            const int i = lane / lanes, k = lane % lanes;
+            const int64_t t = tb + i * step;
+            const bool done = t < t1 && !((open >> i) & 1u), on = done && k < K;
+            const int e = on ? A.slot[i * (K + 1) + k] : 0;
+            const float x = on ? to_f(logits[t * ld + e]) : 0.0f;
+            const float w = lanes == 4 ? weight_of<4>(x, on, A.stats[i], R)
+                            : lanes == 8 ? weight_of<8>(x, on, A.stats[i], R) : weight_of<16>(x, on, A.stats[i], R);
+            if (on) {
+                expert_idx[t * K + k] = e;
+                weights[t * K + k] = w;
+                atomicAdd(&hist[e], 1);
+                if (s_idx) s_idx[t * K + k] = e;
+            } else if (t < t1 && k == 0) {
+                expert_idx[t * K] = -1;  // left open: below
+            }
+            __syncwarp();
         }
     } else {
-        unsure = choose<float, T, LPT, VPL, SCORES>(l, row, bias, R, sm);
-    }
-    if (SCORES && __any_sync(kFull, unsure && valid)) {
-        __syncwarp();
-        choose_again<double, T, LPT, VPL, SCORES>(row, vec, valid, bias, R, slots, nullptr, wide);
-    }
-    float m = 0.0f, z = 1.0f;
-    if (!R.sigmoid && !R.renorm) softmax_stats<float, LPT, VPL>(l, e0, R.E, m, z);
-    const int* slot = slots + tok * (R.K + 1);
-    if (R.renorm) {
-        // ratios: the largest chosen exponent is 0
-        float mx = -INFINITY;
-        for (int k = sub; k < R.K; k += LPT) {
-            const float x = to_f(row[slot[k]]);
-            mx = fmaxf(mx, R.sigmoid ? fminf(x, 0.0f) : x);
+        WarpSmem<float> sm{A.slot, A.slot_v, reinterpret_cast<float*>(A.groups),
+                           reinterpret_cast<float*>(A.groups) + 32 / LPT * padded(LPT * VPL)};
+        for (int64_t t = t0; t - tok < t1; t += step) {
+            const bool valid = t < t1;
+            float l[VPL];
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) l[j] = next[j];
+            const int64_t tn = t + step;
+            load_logits<T, VPL>(logits + (tn < t1 ? tn : 0) * ld, e0, R.E, vec, tn < t1, next);
+            const T* row = logits + (valid ? t : 0) * ld;
+            const bool unsure = choose<float, T, LPT, VPL, MODE>(l, row, bias, R, sm);
+            constexpr unsigned kMine = (1u << LPT) - 1u;
+            const bool open = (__ballot_sync(kFull, unsure) >> (tok * LPT)) & kMine;
+            float2 stats = make_float2(0.0f, 1.0f);
+            if (!R.sigmoid && !R.renorm) softmax_stats<float, LPT, VPL>(l, e0, R.E, stats.x, stats.y);
+            // K experts over LPT lanes, so the sums of a renormalised token take K / LPT turns
+            const int* slot = A.slot + tok * (K + 1);
+            float m = stats.x, z = stats.y;
+            if (R.renorm) {
+                m = -INFINITY;
+                for (int k = sub; k < K; k += LPT) {
+                    const float x = to_f(row[slot[k]]);
+                    m = fmaxf(m, R.sigmoid && x >= 0.0f ? 0.0f : x);
+                }
+                m = lanes_max<LPT>(m);
+                if (m == -INFINITY) m = 0.0f;
+                z = 0.0f;
+                for (int k = sub; k < K; k += LPT) {
+                    const float x = to_f(row[slot[k]]);
+                    const float p = expf((R.sigmoid && x >= 0.0f ? 0.0f : x) - m);
+                    z += R.sigmoid ? p / (1.0f + expf(-fabsf(x))) : p;
+                }
+                z = lanes_sum<LPT>(z);
+                if (z == 0.0f) z = 1.0f;
+            }
+            if (valid && !open) {
+                for (int k = sub; k < K; k += LPT) {
+                    const int e = slot[k];
+                    const float x = to_f(row[e]);
+                    float p = expf((R.sigmoid && x >= 0.0f ? 0.0f : x) - m);
+                    if (R.sigmoid) p = p / (1.0f + expf(-fabsf(x)));
+                    expert_idx[t * K + k] = e;
+                    weights[t * K + k] = R.scale * (p / z);
+                    atomicAdd(&hist[e], 1);
+                    if (s_idx) s_idx[t * K + k] = e;
+                }
+            } else if (valid && sub == 0) {
+                expert_idx[t * K] = -1;
+            }
+            __syncwarp();
         }
-        mx = lanes_max<LPT>(mx);
-        if (mx == -INFINITY) mx = 0.0f;
-        m = mx;
-        float s = 0.0f;
-        for (int k = sub; k < R.K; k += LPT) {
-            const float x = to_f(row[slot[k]]);
-            const float p = expf((R.sigmoid && x >= 0.0f ? 0.0f : x) - m);
-            s += R.sigmoid ? p / (1.0f + expf(-fabsf(x))) : p;
-        }
-        s = lanes_sum<LPT>(s);
-        z = s == 0.0f ? 1.0f : s;
     }
-    for (int k = sub; k < R.K; k += LPT) {
-        const int e = slot[k];
-        const float x = to_f(row[e]);
-        const float p = expf((R.sigmoid && x >= 0.0f ? 0.0f : x) - m);  // m = 0 for the plain sigmoid
-        const float w = (R.sigmoid ? p / (1.0f + expf(-fabsf(x))) : p) / z;
-        if (valid) {
-            expert_idx[t * R.K + k] = e;
-            weights[t * R.K + k] = R.scale * w;
-            atomicAdd(&hist[e], 1);
-            if (s_idx) s_idx[t * R.K + k] = e;
+    // the tokens left open, one after the other; a lane looks at one of the warp's tokens
+    constexpr int TPW = 32 / LPT;
+    const int64_t per_step = TPW, turns = t1 > first ? (t1 - first + step - 1) / step : 0;
+    for (int64_t i0 = 0; i0 < turns * per_step; i0 += 32) {
+        const int64_t i = i0 + lane, t = first + i / per_step * step + i % per_step;
+        const bool mine = i < turns * per_step && t < t1 && expert_idx[t * K] < 0;
+        for (unsigned todo = __ballot_sync(kFull, mine); todo; todo &= todo - 1) {
+            const int64_t tt = __shfl_sync(kFull, t, __ffs(todo) - 1);
+            route_again<T, (LPT == 32 ? VPL : 2), MODE>(logits + tt * ld, tt, vec, bias, R, A.slot, A.slot_v, A.groups, hist,
+                                                        expert_idx, weights, s_idx);
         }
     }
-    __syncwarp();
 }
 
 // Exclusive sums of n <= 256 values (one per thread of the first 256; others pass 0).
@@ -574,7 +735,7 @@ __device__ __forceinline__ void scatter_pairs(const int* idx, int n, int32_t p0,
 
 // ---------------------------------------------------------------- kernels
 // Tokens [b * tpb, (b + 1) * tpb) of block b; blk_counts [gridDim.x][E].
-template <typename T, int LPT, int VPL, bool SCORES>
+template <typename T, int LPT, int VPL, int MODE>
 __global__ void __launch_bounds__(kThreads, 4)
 topk_route_kernel(const T* __restrict__ logits, int64_t ld, int64_t T_, int tpb, bool vec,
                   const float* __restrict__ bias, Rule R, int32_t* __restrict__ expert_idx,
@@ -583,30 +744,20 @@ topk_route_kernel(const T* __restrict__ logits, int64_t ld, int64_t T_, int tpb,
     extern __shared__ __align__(16) uint8_t smem[];
     int* hist = reinterpret_cast<int*>(smem);
     const int warp = threadIdx.x >> 5, tok = (threadIdx.x & 31) / LPT;
-    uint8_t* area = smem + kMaxE * 4 + warp * warp_bytes(R, LPT, VPL);
+    const WarpArea A = warp_area(smem + kMaxE * 4 + warp * warp_bytes(R, LPT, VPL), LPT, R.K);
     constexpr int TPW = 32 / LPT;
     for (int e = threadIdx.x; e < R.E; e += kThreads) hist[e] = 0;
     __syncthreads();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tpb;
     const int64_t t1 = t0 + tpb < T_ ? t0 + tpb : T_;
-    const int e0 = ((threadIdx.x & 31) % LPT) * VPL;
-    float next[VPL];
-    int64_t t = t0 + warp * TPW + tok;
-    load_logits<T, VPL>(logits + (t < t1 ? t : 0) * ld, e0, R.E, vec, t < t1, next);
-    for (; t - tok < t1; t += kWarps * TPW) {
-        float l[VPL];
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) l[j] = next[j];
-        const int64_t tn = t + kWarps * TPW;
-        load_logits<T, VPL>(logits + (tn < t1 ? tn : 0) * ld, e0, R.E, vec, tn < t1, next);
-        route_tokens<T, LPT, VPL, SCORES>(l, logits, ld, t, t < t1, vec, bias, R, area, hist, expert_idx, weights, nullptr);
-    }
+    route_tokens<T, LPT, VPL, MODE>(logits, ld, t0 + warp * TPW + tok, t1, kWarps * TPW, vec, bias, R, A, hist, expert_idx,
+                                    weights, nullptr);
     __syncthreads();
     for (int e = threadIdx.x; e < R.E; e += kThreads) blk_counts[static_cast<int64_t>(blockIdx.x) * R.E + e] = hist[e];
 }
 
 // One block: routes every token, then counts, offsets and perm.
-template <typename T, int LPT, int VPL, bool SCORES>
+template <typename T, int LPT, int VPL, int MODE>
 __global__ void __launch_bounds__(kSmallThreads)
 topk_route_small_kernel(const T* __restrict__ logits, int64_t ld, int T_, bool vec, const float* __restrict__ bias,
                         Rule R, int32_t* __restrict__ expert_idx, float* __restrict__ weights,
@@ -620,14 +771,11 @@ topk_route_small_kernel(const T* __restrict__ logits, int64_t ld, int T_, bool v
     int* s_idx = hist + kMaxE;                                       // [T * K]
     uint8_t* areas = reinterpret_cast<uint8_t*>(s_idx + (T_ * R.K + 3) / 4 * 4);  // slots, then scatter positions
     const int warp = threadIdx.x >> 5, tok = (threadIdx.x & 31) / LPT;
+    const WarpArea A = warp_area(areas + warp * warp_bytes(R, LPT, VPL), LPT, R.K);
     for (int e = threadIdx.x; e < R.E; e += kSmallThreads) hist[e] = 0;
     __syncthreads();
-    for (int t = warp * TPW + tok; t - tok < T_; t += WARPS * TPW) {
-        float l[VPL];
-        load_logits<T, VPL>(logits + static_cast<int64_t>(t < T_ ? t : 0) * ld, ((threadIdx.x & 31) % LPT) * VPL, R.E, vec, t < T_, l);
-        route_tokens<T, LPT, VPL, SCORES>(l, logits, ld, t, t < T_, vec, bias, R, areas + warp * warp_bytes(R, LPT, VPL),
-                                          hist, expert_idx, weights, s_idx);
-    }
+    route_tokens<T, LPT, VPL, MODE>(logits, ld, warp * TPW + tok, T_, WARPS * TPW, vec, bias, R, A, hist, expert_idx, weights,
+                                    s_idx);
     __syncthreads();
     const int e = threadIdx.x;
     const int c = e < R.E ? hist[e] : 0;
@@ -830,9 +978,9 @@ int small_smem(const RouteArgs& a, int warp_area) {
     return smem <= 200 * 1024 ? smem : 0;
 }
 
-template <typename T, int VPL, bool SCORES>
+template <typename T, int VPL, int MODE>
 cudaError_t route_small(const RouteArgs& a, int smem, cudaStream_t s) {
-    auto kernel = topk_route_small_kernel<T, 32, VPL, SCORES>;
+    auto kernel = topk_route_small_kernel<T, 32, VPL, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(1), dim3(kSmallThreads), smem, s, static_cast<const T*>(a.logits), a.ld,
@@ -840,7 +988,7 @@ cudaError_t route_small(const RouteArgs& a, int smem, cudaStream_t s) {
                       a.out.perm);
 }
 
-template <typename T, int LPT, int VPL, bool SCORES>
+template <typename T, int LPT, int VPL, int MODE>
 cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
     const Rule& R = a.R;
     const int wb = warp_bytes(R, LPT, VPL);
@@ -856,7 +1004,7 @@ cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
     const int tpb = static_cast<int>(per) * step;
     const int nblk = static_cast<int>((a.T + tpb - 1) / tpb);
     const int smem = kMaxE * 4 + kWarps * wb;
-    auto kernel = topk_route_kernel<T, LPT, VPL, SCORES>;
+    auto kernel = topk_route_kernel<T, LPT, VPL, MODE>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(nblk), dim3(kThreads), smem, s, static_cast<const T*>(a.logits), a.ld, a.T, tpb, a.vec,
@@ -871,26 +1019,26 @@ cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
 
 // Few tokens: one block, a warp per token (the shortest chain). Many: a token per 1 to 8
 // lanes up to 64 experts, where a warp's rounds serve several tokens, a warp per token above.
-template <typename T, bool SCORES>
+template <typename T, int MODE>
 cudaError_t route_width(const RouteArgs& a, cudaStream_t s) {
     const int E = a.R.E, vpl = E <= 64 ? 2 : E <= 128 ? 4 : 8;
     if (const int smem = small_smem(a, warp_bytes(a.R, 32, vpl))) {
-        if (vpl == 2) return route_small<T, 2, SCORES>(a, smem, s);
-        if (vpl == 4) return route_small<T, 4, SCORES>(a, smem, s);
-        return route_small<T, 8, SCORES>(a, smem, s);
+        if (vpl == 2) return route_small<T, 2, MODE>(a, smem, s);
+        if (vpl == 4) return route_small<T, 4, MODE>(a, smem, s);
+        return route_small<T, 8, MODE>(a, smem, s);
     }
-    if (E <= 8) return route_launch<T, 1, 8, SCORES>(a, s);
-    if (E <= 16) return route_launch<T, 2, 8, SCORES>(a, s);
-    if (E <= 32) return route_launch<T, 4, 8, SCORES>(a, s);
-    if (E <= 64) return route_launch<T, 8, 8, SCORES>(a, s);
-    if (E <= 128) return route_launch<T, 32, 4, SCORES>(a, s);
-    return route_launch<T, 32, 8, SCORES>(a, s);
+    if (E <= 8) return route_launch<T, 1, 8, MODE>(a, s);
+    if (E <= 16) return route_launch<T, 2, 8, MODE>(a, s);
+    if (E <= 32) return route_launch<T, 4, 8, MODE>(a, s);
+    if (E <= 64) return route_launch<T, 8, 8, MODE>(a, s);
+    if (E <= 128) return route_launch<T, 32, 4, MODE>(a, s);
+    return route_launch<T, 32, 8, MODE>(a, s);
 }
 
 template <typename T>
 cudaError_t route_type(const RouteArgs& a, cudaStream_t s) {
     const bool scores = a.bias || (a.R.G > 1 && a.R.best == 2);
-    return scores ? route_width<T, true>(a, s) : route_width<T, false>(a, s);
+    return !scores ? route_width<T, kLogits>(a, s) : a.R.sigmoid ? route_width<T, kSigmoid>(a, s) : route_width<T, kSoftmax>(a, s);
 }
 
 template <typename T>
