@@ -125,10 +125,12 @@ __device__ __forceinline__ void load_logits(const T* row, int e0, int E, bool ve
     }
 }
 
+// The bias of a lane's experts, NaN past the last one: what is no expert is then NaN in
+// every value that is compared.
 template <int VPL>
 __device__ __forceinline__ void load_bias(const float* bias, int e0, int E, float (&b)[VPL]) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) b[j] = bias && e0 + j < E ? bias[e0 + j] : 0.0f;
+    for (int j = 0; j < VPL; ++j) b[j] = e0 + j >= E ? __int_as_float(0x7fffffff) : bias ? bias[e0 + j] : 0.0f;
 }
 
 __device__ __forceinline__ bool is_masked(float l) { return !(l > -INFINITY); }
@@ -327,7 +329,7 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
 template <typename T, int VPL, int MODE>
 __device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const float (&b)[VPL], const T* row,
                                                     const float* __restrict__ bias, const Rule& R, int* slot,
-                                                    float* slot_v, float2* cand, int* found, float* groups, float2& stats,
+                                                    float* slot_v, uint2* cand, int* found, float* groups, float2& stats,
                                                     float& guess) {
     const int lane = threadIdx.x & 31, e0 = lane * VPL;
     const float nan = __int_as_float(0x7fffffff);
@@ -337,17 +339,16 @@ __device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const
     if (MODE == kSoftmax || (!R.sigmoid && !R.renorm)) softmax_stats<float, 32, VPL>(l, e0, R.E, stats.x, stats.y);
     if (MODE == kLogits) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) order[j] = is_masked(l[j]) ? -INFINITY : l[j];
+        for (int j = 0; j < VPL; ++j) order[j] = is_masked(l[j]) ? -INFINITY : l[j] + b[j];
     } else {
         const float inv_z = MODE == kSoftmax ? 1.0f / stats.y : 1.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
-            const float s = (MODE == kSigmoid ? sigmoid_v(l[j]) : expf(l[j] - stats.x) * inv_z) + b[j];
-            order[j] = l[j] > -INFINITY && (MODE == kSigmoid || s == s) ? s : -INFINITY;
+            const float s = MODE == kSigmoid ? sigmoid_v(l[j]) : expf(l[j] - stats.x) * inv_z;
+            order[j] = l[j] > -INFINITY && (MODE == kSigmoid || s == s) ? s + b[j] : -INFINITY;
         }
     }
     bool keep = true;
-    unsigned alive = 0xffffffffu;
     if (R.G > 1) {
         const int L = R.S / VPL;  // lanes a group spans
         if (R.S % VPL == 0 && (L & (L - 1)) == 0) {
@@ -387,29 +388,31 @@ __device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const
         } else {
             unsigned kept;
             unsure = group_kept<float, 32, VPL, MODE>(order, e0, 0, R, groups, groups + padded(32 * VPL), tol, kept);
-            alive = group_alive<VPL>(kept, e0, R);
+            const unsigned alive = group_alive<VPL>(kept, e0, R);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (!((alive >> j) & 1u)) order[j] = nan;
+            keep = alive != 0;
         }
     }
     const bool check = MODE != kLogits && bias;
     if (MODE != kLogits && !bias) {  // groups were chosen by scores, experts are by logits
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) order[j] = is_masked(l[j]) ? -INFINITY : l[j];
+        for (int j = 0; j < VPL; ++j)
+            if (order[j] == order[j]) order[j] = is_masked(l[j]) ? -INFINITY : l[j];
     }
-    const int mine_n = keep ? R.E - e0 : 0;  // experts of this lane that count
     const int need = check ? R.K + 1 : R.K;
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-        if (j >= mine_n || !((alive >> j) & 1u)) order[j] = nan;
-        n += order[j] >= guess ? 1 : 0;
-    }
+    for (int j = 0; j < VPL; ++j) n += order[j] >= guess ? 1 : 0;
+    if (!keep) n = 0;
     float tau = guess;
     int total = __reduce_add_sync(kFull, n);
     if (total < need || total > 32) {
         float top = nan;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) top = fmaxf(top, order[j]);
-        uint32_t cur = top != top ? 0u : key_of(top);
+        uint32_t cur = !keep || top != top ? 0u : key_of(top);
         tau = -INFINITY;
         for (int reached = 0;;) {
             const uint32_t mx = __reduce_max_sync(kFull, cur);
@@ -425,34 +428,36 @@ __device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const
         n = 0;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) n += order[j] >= tau ? 1 : 0;
+        if (!keep) n = 0;
         total = __reduce_add_sync(kFull, n);
         if (total > 32) return false;
     }
-    // the list's order does not matter: its entries are ranked by value and index
+    // the list's order does not matter: its entries are ranked by value and index, as one
+    // 64-bit number each
     if (n) {
         int at = atomicAdd(found, n);
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
-            if (order[j] >= tau) cand[at++] = make_float2(order[j], __int_as_float(e0 + j));
+            if (order[j] >= tau) cand[at++] = make_uint2(static_cast<uint32_t>(~(e0 + j)), __float_as_uint(order[j]));
     }
     __syncwarp();
     if (lane == 0) *found = 0;
-    const float2 mine = lane < total ? cand[lane] : make_float2(nan, 0.0f);
-    const int my_e = __float_as_int(mine.y);
+    const uint2 mine = lane < total ? cand[lane] : make_uint2(0u, 0u);
+    const float my_v = __uint_as_float(mine.y);
+    const uint64_t my_key = (static_cast<uint64_t>(key_of(my_v)) << 32) | mine.x;
+    if (lane < total) reinterpret_cast<uint64_t*>(cand)[lane] = my_key;
+    __syncwarp();
     int rank = 0;
 #pragma unroll 4
-    for (int o = 0; o < total; ++o) {
-        const float2 c = cand[o];
-        rank += (c.x > mine.x || (c.x == mine.x && __float_as_int(c.y) < my_e)) ? 1 : 0;
+    for (int o = 0; o < total; ++o) rank += reinterpret_cast<const uint64_t*>(cand)[o] > my_key ? 1 : 0;
+    if (lane < total && rank < need) {
+        slot[rank] = static_cast<int>(~mine.x);
+        slot_v[rank] = my_v;
     }
-    const bool in = lane < total && rank < need;
-    if (in) {
-        slot[rank] = my_e;
-        slot_v[rank] = mine.x;
-    }
-    // the next token's guess: the value a few places behind the last one needed
+    // the next token's guess follows the value a few places behind the last one needed
     const unsigned b_guess = __ballot_sync(kFull, lane < total && rank == min(total - 1, need + 4));
-    guess = __shfl_sync(kFull, mine.x, __ffs(b_guess) - 1);
+    const float at_guess = __shfl_sync(kFull, my_v, __ffs(b_guess) - 1);
+    guess = guess == guess && fabsf(guess) < INFINITY ? guess + 0.25f * (at_guess - guess) : at_guess;
     if (check) {
         __syncwarp();
         if (lane < R.K && lane + 1 < total) {
@@ -527,7 +532,7 @@ struct WarpArea {
     int* slot;
     float* slot_v;
     float2* stats;
-    float2* cand;
+    uint2* cand;
     int* found;  // zero between tokens
     double* groups;
 };
@@ -549,7 +554,7 @@ __device__ __forceinline__ WarpArea warp_area(uint8_t* p, int lpt, int K) {
     a.slot = reinterpret_cast<int*>(p);
     a.slot_v = reinterpret_cast<float*>(p + n * (K + 1) * 4);
     a.stats = reinterpret_cast<float2*>(p + n * (K + 1) * 8);
-    a.cand = a.stats + n;
+    a.cand = reinterpret_cast<uint2*>(a.stats + n);
     a.found = reinterpret_cast<int*>(a.cand + 32);
     a.groups = reinterpret_cast<double*>(a.found + 2);
     return a;
