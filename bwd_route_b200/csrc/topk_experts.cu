@@ -86,6 +86,21 @@ __device__ __forceinline__ uint4 pack8(const float (&s)[8]) {
     return v;
 }
 
+// Division of pair numbers (below 2^31) by K: q = (p * mul) >> shift, exact for
+// shift = 31 + ceil(log2 K), mul = floor(2^shift / K) + 1.
+struct DivK {
+    uint32_t mul;
+    int shift;
+    __device__ __forceinline__ int operator()(int p) const {
+        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(p)) * mul) >> shift);
+    }
+};
+inline DivK div_by(int K) {
+    int s = 0;
+    while ((1 << s) < K) ++s;
+    return {static_cast<uint32_t>((uint64_t{1} << (31 + s)) / static_cast<uint32_t>(K) + 1), 31 + s};
+}
+
 __device__ __forceinline__ void st_shared_u4(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -163,6 +178,7 @@ struct PairArgs {
     const int32_t* offsets;
     const int32_t* perm;
     int E, K, H;
+    DivK by_k;
     int64_t P;
     void* out;             // [T][H]; d_x: may be NULL (only the weights' gradient)
     __half* rows;          // [P][H], K > 1
@@ -232,21 +248,27 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
         const int ptid = threadIdx.x - kPProducer0;
         const int prow = ptid >> 3, pg = ptid & 7;
         int tok[8], nxt[8];
-        auto load_tokens = [&](int tile, int (&t)[8]) {
+        // the pairs of a tile's rows; their tokens are worked out a tile later, when the loads are there
+        auto load_pairs = [&](int tile, int (&t)[8]) {
             int e, row0, nrows;
             tile_rows(tile, e, row0, nrows);
 #pragma unroll
             for (int it = 0; it < 8; ++it) {
                 const int r = it * 16 + prow;
-                t[it] = r < nrows ? A.perm[row0 + r] / K : -1;
+                t[it] = r < nrows ? A.perm[row0 + r] : -1;
             }
         };
-        if (static_cast<int>(blockIdx.x) < ntiles) load_tokens(blockIdx.x, tok);
+        auto to_tokens = [&](const int (&pair)[8]) {
+#pragma unroll
+            for (int it = 0; it < 8; ++it) tok[it] = pair[it] < 0 ? -1 : A.by_k(pair[it]);
+        };
+        if (static_cast<int>(blockIdx.x) < ntiles) load_pairs(blockIdx.x, nxt);
+        to_tokens(nxt);
         int sa = 0;
         uint32_t pa = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-            if (tile + static_cast<int>(gridDim.x) < ntiles) load_tokens(tile + gridDim.x, nxt);
+            if (tile + static_cast<int>(gridDim.x) < ntiles) load_pairs(tile + gridDim.x, nxt);
             for (int kc = 0; kc < KCH; ++kc) {
                 if (!(ok = mbar_wait(&ctl->aempty[sa], pa ^ 1, abort, A.flags))) break;
                 const uint32_t a_u32 = smem_u32(aring + sa * C::A_BYTES);
@@ -263,8 +285,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                     pa ^= 1;
                 }
             }
-#pragma unroll
-            for (int it = 0; it < 8; ++it) tok[it] = nxt[it];
+            to_tokens(nxt);
         }
     } else if (warp == kPLoadWarp) {
         // ---------------- weight loader. Boxes may reach past the expert's last row or column block
@@ -364,7 +385,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                 const int R = it * 8 + R4;
                 const int pr = __shfl_sync(kFull, pair, R);
                 cp_async_16(my + buf * C::STEP_BYTES + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4),
-                            xs + static_cast<int64_t>(pr < 0 ? 0 : pr / K) * H + col + j4 * 8, pr < 0 ? 0u : 16u);
+                            xs + static_cast<int64_t>(pr < 0 ? 0 : A.by_k(pr)) * H + col + j4 * 8, pr < 0 ? 0u : 16u);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -591,6 +612,7 @@ struct WgradArgs {
     const int32_t* offsets;
     const int32_t* perm;
     int E, K, H, extra;
+    DivK by_k;
     int64_t P;
     void* dW;       // may be NULL (db only)
     void* db;       // may be NULL
@@ -621,7 +643,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
     uint8_t* stg = smem + C::STAGES * C::STAGE;
     WCtl* ctl = reinterpret_cast<WCtl*>(smem + C::STAGES * C::STAGE + C::STG);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int H = A.H, K = A.K;
+    const int H = A.H;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&ctl->raw[s], 128);  // the gather threads' copies
@@ -674,14 +696,16 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
             const Unit r = unit_of(u);
             const bool on_g = lane * 8 < min(kWTile, H - r.o0), on_x = lane * 8 < min(kWTile, H - r.i0);
-            // this warp's 8 rows of a stage are w4, w4 + 4, ...; lane i < 8 looks row i up, a stage ahead
+            // this warp's 8 rows of a stage are w4, w4 + 4, ...; lane i < 8 looks row i up, two stages ahead
             auto look = [&](int p0) {
                 const int i = p0 + w4 + 4 * (lane & 7);
-                return i < r.hi ? A.perm[i] / K : -1;
+                return i < r.hi ? A.perm[i] : -1;
             };
-            int tok = look(r.lo);
+            int pair = look(r.lo), npair = look(r.lo + C::KT);
             for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
-                const int ntok = look(p0 + C::KT);
+                const int tok = pair < 0 ? -1 : A.by_k(pair);
+                pair = npair;
+                npair = look(p0 + 2 * C::KT);
                 if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
                 const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
 #pragma unroll
@@ -698,7 +722,6 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                     stage = 0;
                     phase ^= 1;
                 }
-                tok = ntok;
             }
         }
     } else if (warp == kWMmaWarp) {
@@ -1102,6 +1125,7 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
     a.perm = routing->perm;
     a.E = E;
     a.K = K;
+    a.by_k = div_by(K);
     a.H = H;
     a.P = static_cast<int64_t>(P);
     a.out = y;
@@ -1158,6 +1182,7 @@ moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dt
     a.perm = routing->perm;
     a.E = E;
     a.K = K;
+    a.by_k = div_by(K);
     a.H = H;
     a.P = static_cast<int64_t>(P);
     a.out = d_x;
@@ -1173,6 +1198,7 @@ moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dt
     g.perm = routing->perm;
     g.E = E;
     g.K = K;
+    g.by_k = a.by_k;
     g.H = H;
     g.extra = wgrad_extra(E, H);
     g.P = static_cast<int64_t>(P);
