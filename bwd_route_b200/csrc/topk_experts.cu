@@ -18,8 +18,8 @@
 //     [2^14, 2^15)): half of fp32's traffic at 11 bits, finer than bf16's 8, whatever the
 //     magnitude. The backward's epilogue also takes x . (W_e^T g) from the fp32
 //     accumulators, with its warps' rows of x brought in by cp.async beside them.
-//   join_kernel   : adds the K rows of a token in the order of k in fp32, one rounding;
-//     in the backward also d_w from the column parts and g . b_e.
+//   join_kernel   : adds the K rows of a token (and w b_e) in the order of k in fp32, one
+//     rounding; in the backward also d_w from the column parts and g . b_e.
 //   wgrad_kernel  : dW and db. The pairs are the contraction index: both operands are
 //     MN-major. Four warps gather rows of g and x by cp.async, eight scale the staged rows
 //     of g by w in place (rounded to the operand type) and add them up for db; a unit is a
@@ -189,7 +189,8 @@ struct PairArgs {
 
 // DX = false: B_e[n][k] = W[e][n][k], K-major. DX = true: B_e[n][k] = W[e][k][n], MN-major
 // straight from W.
-template <typename T, int BN, bool DX>
+// ONE: K = 1, a pair's row is the result.
+template <typename T, int BN, bool DX, bool ONE>
 __global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
     using C = PairCfg<BN, DX>;
@@ -200,7 +201,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
     uint8_t* stg = smem + C::RING_BYTES;
     PairCtl* ctl = reinterpret_cast<PairCtl*>(smem + C::RING_BYTES + C::STG_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int H = A.H, K = A.K;
+    const int H = A.H;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::A_STAGES; ++s) {
@@ -400,26 +401,50 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
             const float w = p >= 0 ? A.weights[p] : 0.0f;
             if (next_tile < ntiles) p_next = tile_pair(next_tile);
             const int nt = tile % NT, col0 = nt * BN + half * HALF, ncols = tile_cols(tile);
-            const int e = span_of(ctl->tstart, A.E, tile / NT);
+            const int e = ONE && !DX ? span_of(ctl->tstart, A.E, tile / NT) : 0;  // for the bias
             if (!mbar_wait(&ctl->tfull[acc], acc_phase, abort, A.flags)) break;
             __syncwarp();
             tc_fence_after();
             const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(acc * BN + half * HALF);
+            // where the lane's share of rows 8 it + R4 goes: the output, or rows of the workspace
+            uint8_t* dst[4];
+            unsigned there = 0;
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int pr = __shfl_sync(kFull, p, it * 8 + R4);
+                there |= pr >= 0 ? 1u << it : 0u;
+                dst[it] = (ONE ? reinterpret_cast<uint8_t*>(out) : reinterpret_cast<uint8_t*>(A.rows)) +
+                          (static_cast<int64_t>(pr < 0 ? 0 : pr) * H + col0 + j4 * 8) * 2;
+            }
             float dot = 0.0f;
-            for (int c = 0; c < ncols; c += 32) {
-                float v[32];
-                tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c), v);
-                if (c + 32 >= ncols) {  // the accumulator is read: the next tile may have it
+            float inv[HALF / 32];  // this lane's row: the powers its blocks were divided by
+            uint32_t tm[2][32];
+            if (ncols > 0) {
+                tmem_ld_32x32b_x32_async(tbase, tm[0]);
+                tmem_ld_wait_tied(tm[0]);
+            }
+#pragma unroll
+            for (int i = 0; i < HALF / 32; ++i) {
+                const int c = 32 * i;
+                if (c >= ncols) break;
+                const bool more = c + 32 < ncols;
+                // the next step's sums on the way; after the last the next tile may have the accumulator
+                if (more) {
+                    tmem_ld_32x32b_x32_async(tbase + static_cast<uint32_t>(c + 32), tm[(i + 1) & 1]);
+                } else {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->tempty[acc]);
                 }
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(tm[i & 1][j]);
                 const int col = col0 + c;
                 const uint32_t stage = my + (DX ? buf * C::STEP_BYTES : 0);
+                bool store = true;
                 if (DX) {
                     if (A.other) {
                         // the next step's rows of x (of this tile or the next) on the way, this one's here
-                        const bool more = c + 32 < ncols;
                         if (more) fetch_x(p, col + 32, buf ^ 1);
                         else if (next_tile < ntiles && tile_cols(next_tile) > 0)
                             fetch_x(p_next, (next_tile % NT) * BN + half * HALF, buf ^ 1);
@@ -431,54 +456,59 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                             const uint4 raw = ld_shared_u4(stage + lane * 64 + ((g ^ swz) << 4));
                             const T* xv = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) dot += v[8 * g + i] * to_f(xv[i]);
+                            for (int j = 0; j < 8; ++j) dot += v[8 * g + j] * to_f(xv[j]);
                         }
                     }
                     buf ^= 1;
-                    if (!out) {
-                        __syncwarp();
-                        continue;
-                    }
-                } else if (A.bias) {
+                    store = out != nullptr;
+                } else if (ONE && A.bias) {
                     const T* br = static_cast<const T*>(A.bias) + static_cast<int64_t>(e) * H + col;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br + 8 * g);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[8 * g + i] += to_f(bv.v[i]);
+                        for (int j = 0; j < 8; ++j) v[8 * g + j] += to_f(bv.v[j]);
                     }
                 }
-                float f = w;
-                if (K > 1) {
-                    float m = 0.0f;
+                if (store) {
+                    float f = w;
+                    if (!ONE) {
+                        float m = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
-                    // exponent of the largest |v w|, 40 at least: fp16's last step is then 2^-125
-                    const int ex = max(static_cast<int>((__float_as_uint(m * fabsf(w)) >> 23) & 255), 40);
-                    f = w * __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
-                    f = fminf(fmaxf(f, -3e38f), 3e38f);  // only where |v w| is below 2^-87
-                    if (p >= 0) A.scale[static_cast<int64_t>(p) * (H / 32) + (col >> 5)] = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
-                }
+                        for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[j]));
+                        // exponent of the largest |v w|, 40 at least: fp16's last step is then 2^-125
+                        const int ex = max(static_cast<int>((__float_as_uint(m * fabsf(w)) >> 23) & 255), 40);
+                        f = w * __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+                        f = fminf(fmaxf(f, -3e38f), 3e38f);  // only where |v w| is below 2^-87
+                        inv[i] = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
+                    }
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float s[8];
+                    for (int g = 0; g < 4; ++g) {
+                        float s[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[i] = v[8 * g + i] * f;
-                    st_shared_u4(stage + lane * 64 + ((g ^ swz) << 4), K > 1 ? pack8<__half>(s) : pack8<T>(s));
-                }
-                __syncwarp();
+                        for (int j = 0; j < 8; ++j) s[j] = v[8 * g + j] * f;
+                        st_shared_u4(stage + lane * 64 + ((g ^ swz) << 4), ONE ? pack8<T>(s) : pack8<__half>(s));
+                    }
+                    __syncwarp();
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const int R = it * 8 + R4;
-                    const uint4 val = ld_shared_u4(stage + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4));
-                    const int pr = __shfl_sync(kFull, p, R);
-                    const int64_t at = static_cast<int64_t>(pr) * H + col + j4 * 8;
-                    if (pr >= 0) {
-                        if (K > 1) *reinterpret_cast<uint4*>(A.rows + at) = val;
-                        else *reinterpret_cast<uint4*>(out + at) = val;
+                    for (int it = 0; it < 4; ++it) {
+                        const int R = it * 8 + R4;
+                        const uint4 val = ld_shared_u4(stage + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4));
+                        if ((there >> it) & 1u) *reinterpret_cast<uint4*>(dst[it] + 2 * c) = val;
                     }
                 }
                 __syncwarp();
+                if (more) tmem_ld_wait_tied(tm[(i + 1) & 1]);
+            }
+            if (!ONE && p >= 0 && ncols > 0 && (!DX || out)) {
+                float* sc = A.scale + static_cast<int64_t>(p) * (H / 32) + (col0 >> 5);
+                if (HALF == 128 && ncols == 128 && H % 128 == 0) {  // 16-byte aligned
+                    *reinterpret_cast<float4*>(sc) = make_float4(inv[0], inv[1 % (HALF / 32)], inv[2 % (HALF / 32)], inv[3 % (HALF / 32)]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < HALF / 32; ++i)
+                        if (32 * i < ncols) sc[i] = inv[i];
+                }
             }
             if (ncols <= 0) {
                 __syncwarp();
@@ -508,72 +538,90 @@ struct JoinArgs {
     void* out;             // [T][H], or NULL
     const float* dw_part;  // [parts][P]; d_weights only
     int parts;
-    const void* g;         // [T][H], with bias
-    const void* bias;      // [E][H] or NULL
+    const void* g;         // [T][H]: d_weights, with bias
+    const void* bias;      // [E][H] or NULL: added to the forward's rows, part of d_weights
     const int32_t* expert_idx;
-    float* d_weights;      // [P] or NULL
+    const float* weights;  // [P]: forward, with bias
+    float* d_weights;      // [P] or NULL (the forward)
     int64_t T;
     int K, H;
 };
 
-// LPT lanes per token, 8 columns each at a time; KM: an upper bound of K.
-template <typename T, int KM>
+// LPT lanes per token, 8 columns each at a time; U tokens per turn, so that enough loads
+// are on the way; KM: an upper bound of K. DW: the backward (d_weights may be NULL).
+template <typename T, int KM, int U, bool DW>
 __global__ void __launch_bounds__(256) join_kernel(const JoinArgs A, int LPT) {
     griddep_wait();  // every global access below comes after the previous grid
-    const int lane = threadIdx.x & 31, sub = lane % LPT, K = A.K, H = A.H;
+    const int lane = threadIdx.x & 31, sub = lane % LPT, K = A.K, H = A.H, per_warp = 32 / LPT;
     const int64_t P = A.T * K;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * (32 / LPT);
+    const bool with_bias = A.bias != nullptr, rows = A.out != nullptr;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * per_warp * U;
     // a warp's tokens run in step: lanes past the last token only take part in the shuffles
-    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (32 / LPT); base < A.T; base += step) {
-        const int64_t t = base + lane / LPT;
-        const bool valid = t < A.T;
-        float dot[KM];
-        const T* br[KM];
-        const bool with_bias = A.d_weights && A.bias;
+    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * per_warp * U; base < A.T; base += step) {
+        int64_t t[U];
+        const T* br[U][KM];
+        float wk[U][KM], dot[U][KM];
 #pragma unroll
-        for (int k = 0; k < KM; ++k) {
-            dot[k] = 0.0f;
-            br[k] = with_bias && valid && k < K ? static_cast<const T*>(A.bias) + static_cast<int64_t>(A.expert_idx[t * K + k]) * H : nullptr;
-        }
-        for (int c = sub * 8; valid && c < H; c += LPT * 8) {
-            if (A.out) {
-                Chunk<__half, 8> r[KM];
-                float f[KM];
-#pragma unroll
-                for (int k = 0; k < KM; ++k)
-                    if (k < K) {
-                        r[k] = *reinterpret_cast<const Chunk<__half, 8>*>(A.rows + (t * K + k) * H + c);
-                        f[k] = A.scale[(t * K + k) * (H / 32) + (c >> 5)];
-                    }
-                float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < KM; ++k)
-                    if (k < K)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) s[i] = fmaf(to_f(r[k].v[i]), f[k], s[i]);
-                *reinterpret_cast<uint4*>(static_cast<T*>(A.out) + t * H + c) = pack8<T>(s);
-            }
-            if (with_bias) {
-                const Chunk<T, 8> gv = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.g) + t * H + c);
-#pragma unroll
-                for (int k = 0; k < KM; ++k)
-                    if (k < K) {
-                        const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br[k] + c);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dot[k] += to_f(gv.v[i]) * to_f(bv.v[i]);
-                    }
-            }
-        }
-        if (A.d_weights) {
+        for (int u = 0; u < U; ++u) {
+            t[u] = base + u * per_warp + lane / LPT;
 #pragma unroll
             for (int k = 0; k < KM; ++k) {
-                if (k < K) {
-                    if (valid)
-                        for (int i = sub; i < A.parts; i += LPT) dot[k] += A.dw_part[i * P + t * K + k];
-                    for (int off = LPT / 2; off >= 1; off >>= 1) dot[k] += __shfl_xor_sync(kFull, dot[k], off);
-                    if (valid && sub == 0) A.d_weights[t * K + k] = dot[k];
-                }
+                const bool on = with_bias && t[u] < A.T && k < K;
+                br[u][k] = static_cast<const T*>(A.bias) + (on ? static_cast<int64_t>(A.expert_idx[t[u] * K + k]) * H : 0);
+                wk[u][k] = !DW && on ? A.weights[t[u] * K + k] : 0.0f;
+                dot[u][k] = 0.0f;
             }
+        }
+        for (int c = sub * 8; c < H; c += LPT * 8) {
+            Chunk<__half, 8> r[U][KM];
+            float f[U][KM];
+            Chunk<T, 8> gv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t[u] >= A.T) continue;
+                if (rows)
+#pragma unroll
+                    for (int k = 0; k < KM; ++k)
+                        if (k < K) {
+                            r[u][k] = *reinterpret_cast<const Chunk<__half, 8>*>(A.rows + (t[u] * K + k) * H + c);
+                            f[u][k] = A.scale[(t[u] * K + k) * (H / 32) + (c >> 5)];
+                        }
+                if (DW && with_bias) gv[u] = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.g) + t[u] * H + c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t[u] >= A.T) continue;
+                float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < KM; ++k) {
+                    if (k >= K) continue;
+                    if (rows)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s[i] = fmaf(to_f(r[u][k].v[i]), f[u][k], s[i]);
+                    if (with_bias) {
+                        const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br[u][k] + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (DW) dot[u][k] += to_f(gv[u].v[i]) * to_f(bv.v[i]);
+                            else s[i] = fmaf(to_f(bv.v[i]), wk[u][k], s[i]);
+                        }
+                    }
+                }
+                if (rows) *reinterpret_cast<uint4*>(static_cast<T*>(A.out) + t[u] * H + c) = pack8<T>(s);
+            }
+        }
+        if (DW && A.d_weights) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < KM; ++k) {
+                    if (k >= K) continue;
+                    float d = dot[u][k];
+                    if (t[u] < A.T)
+                        for (int i = sub; i < A.parts; i += LPT) d += A.dw_part[i * P + t[u] * K + k];
+                    for (int off = LPT / 2; off >= 1; off >>= 1) d += __shfl_xor_sync(kFull, d, off);
+                    if (t[u] < A.T && sub == 0) A.d_weights[t[u] * K + k] = d;
+                }
         }
     }
 }
@@ -978,7 +1026,7 @@ cudaError_t pair_launch(const void* W, moe_dtype_t dtype, const PairArgs& a, int
     using C = PairCfg<BN, DX>;
     CUtensorMap map;
     if (!weight_map(&map, W, dtype, static_cast<uint64_t>(a.E) * a.H, a.H, DX ? 64 : BN)) return cudaErrorInvalidValue;
-    auto kernel = pair_kernel<T, BN, DX>;
+    auto kernel = a.K == 1 ? pair_kernel<T, BN, DX, true> : pair_kernel<T, BN, DX, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     const int nt = (a.H + BN - 1) / BN;
@@ -1003,20 +1051,23 @@ cudaError_t pair_width(const void* W, moe_dtype_t dtype, const PairArgs& a, int 
     return pair_launch<T, 64, DX>(W, dtype, a, sms, s, parts);
 }
 
-template <typename T>
+template <typename T, bool DW>
 cudaError_t join_launch(const JoinArgs& a, int sms, cudaStream_t s) {
     int lpt = 8;
     while (lpt < 32 && lpt * 8 < a.H) lpt *= 2;
-    const int64_t tokens = 8 * (32 / lpt), want = (a.T + tokens - 1) / tokens, cap = static_cast<int64_t>(sms) * 16;
-    const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
-    if (a.K <= 2) return launch_pdl(join_kernel<T, 2>, grid, dim3(256), 0, s, a, lpt);
-    if (a.K <= 4) return launch_pdl(join_kernel<T, 4>, grid, dim3(256), 0, s, a, lpt);
-    if (a.K <= 8) return launch_pdl(join_kernel<T, 8>, grid, dim3(256), 0, s, a, lpt);
-    return launch_pdl(join_kernel<T, 16>, grid, dim3(256), 0, s, a, lpt);
+    auto go = [&](auto kernel, int u) {
+        const int64_t tokens = 8 * (32 / lpt) * u, want = (a.T + tokens - 1) / tokens, cap = static_cast<int64_t>(sms) * 8;
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s, a, lpt);
+    };
+    if (a.K <= 2) return go(join_kernel<T, 2, 2, DW>, 2);
+    if (a.K <= 4) return go(join_kernel<T, 4, 1, DW>, 1);
+    if (a.K <= 8) return go(join_kernel<T, 8, 1, DW>, 1);
+    return go(join_kernel<T, 16, 1, DW>, 1);
 }
 
 template <typename T>
-cudaError_t fwd_type(const void* W, moe_dtype_t dtype, const PairArgs& a, int64_t T_, int sms, cudaStream_t s) {
+cudaError_t fwd_type(const void* W, moe_dtype_t dtype, const PairArgs& a, int64_t T_, const int32_t* expert_idx, int sms,
+                     cudaStream_t s) {
     int parts = 0;
     cudaError_t e = pair_width<T, false>(W, dtype, a, sms, s, &parts);
     if (e != cudaSuccess || a.K == 1) return e;
@@ -1024,10 +1075,13 @@ cudaError_t fwd_type(const void* W, moe_dtype_t dtype, const PairArgs& a, int64_
     j.rows = a.rows;
     j.scale = a.scale;
     j.out = a.out;
+    j.bias = a.bias;
+    j.expert_idx = expert_idx;
+    j.weights = a.weights;
     j.T = T_;
     j.K = a.K;
     j.H = a.H;
-    return join_launch<T>(j, sms, s);
+    return join_launch<T, false>(j, sms, s);
 }
 
 template <typename T>
@@ -1074,7 +1128,7 @@ cudaError_t bwd_type(const void* W, const void* bias, moe_dtype_t dtype, PairArg
             j.T = T_;
             j.K = a.K;
             j.H = a.H;
-            e = join_launch<T>(j, sms, s);
+            e = join_launch<T, true>(j, sms, s);
         }
     }
     if (e == cudaSuccess && (wg.dW || wg.db)) e = wgrad_launch<T>(wg, sms, s);
@@ -1101,14 +1155,16 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
     if (st != MOE_OK) return st;
     if (!routing || !W) return MOE_ERR_INVALID_ARG;
     if (T > 0 && (!x || !y || !weights || !routing->offsets || !routing->perm)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && K > 1 && bias && !routing->expert_idx) return MOE_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(W, 16) || !aligned(bias, 16) || !aligned(y, 16) || !aligned(weights, 4) ||
-        !aligned(routing->offsets, 4) || !aligned(routing->perm, 4))
+        !aligned(routing->offsets, 4) || !aligned(routing->perm, 4) || !aligned(routing->expert_idx, 4))
         return MOE_ERR_MISALIGNED;
     const size_t P = static_cast<size_t>(T) * K, act = 2 * static_cast<size_t>(T) * H;
     const Range outs[2] = {{y, act}, {workspace, workspace ? workspace_bytes : 0}};
-    const Range ins[6] = {{x, act}, {W, 2 * static_cast<size_t>(E) * H * H}, {bias, 2 * static_cast<size_t>(E) * H},
-                          {weights, 4 * P}, {routing->offsets, sizeof(int32_t) * (E + 1)}, {routing->perm, 4 * P}};
-    if (any_alias(outs, 2, ins, 6)) return MOE_ERR_ALIAS;
+    const Range ins[7] = {{x, act}, {W, 2 * static_cast<size_t>(E) * H * H}, {bias, 2 * static_cast<size_t>(E) * H},
+                          {weights, 4 * P}, {routing->offsets, sizeof(int32_t) * (E + 1)}, {routing->perm, 4 * P},
+                          {routing->expert_idx, 4 * P}};
+    if (any_alias(outs, 2, ins, 7)) return MOE_ERR_ALIAS;
     if (T == 0) return MOE_OK;
     const ExpertsWs L = experts_ws(T, E, K, H, topk_route_ws_bytes(T, E));
     if (!workspace) return MOE_ERR_WORKSPACE;
@@ -1133,8 +1189,8 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
     a.scale = reinterpret_cast<float*>(ws + L.scale);
     a.flags = reinterpret_cast<uint32_t*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(dtype == MOE_DTYPE_BF16 ? fwd_type<__nv_bfloat16>(W, dtype, a, T, sms, s)
-                                               : fwd_type<__half>(W, dtype, a, T, sms, s));
+    return cuda_status(dtype == MOE_DTYPE_BF16 ? fwd_type<__nv_bfloat16>(W, dtype, a, T, routing->expert_idx, sms, s)
+                                               : fwd_type<__half>(W, dtype, a, T, routing->expert_idx, sms, s));
 }
 
 moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dtype_t dtype, const void* d_out,

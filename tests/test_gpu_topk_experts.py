@@ -3,8 +3,9 @@
 Tolerances. u = 2^-24, r = eps(type) / 2. A tensor-core sum over n terms adds 16 at a
 time to an fp32 accumulator, each addition off by at most 2^-22 of the largest
 magnitude in it: A(n) = (n / 16 + 8) 2^-22 of the sum of the terms' magnitudes.
-  y, d_x: A(H) of the magnitudes; when K > 1 every row is rounded to fp16 scaled to its
-  block's largest value, 2^-11 of itself and 2^-39 of that value; r of the result.
+  y, d_x: A(H) of the magnitudes; when K > 1 every row w W x (the bias is added after it,
+  in fp32) is rounded to fp16 scaled to its block's largest value, 2^-11 of itself and
+  2^-39 of that value; r of the result.
   d_weights: A(H) of the magnitudes for the inner sum, 2 H u of them for the outer.
   dW: the rows w g are rounded to the type, independent errors of at most r of each
   term, so beyond 8 r sqrt(sum of squares) with probability below 2 exp(-32) per
@@ -70,9 +71,10 @@ def _reference(x, W, b, g, idx, w):
         if t.numel() == 0:
             continue
         wt = w[t, k][:, None]
-        row = x[t] @ W[e].T + b[e]
+        plain = x[t] @ W[e].T
+        row = plain + b[e]
         o["y"].index_add_(0, t, wt * row)
-        o["y_rows"].index_add_(0, t, (wt * row).abs())
+        o["y_rows"].index_add_(0, t, (wt * plain).abs())
         o["y_acc"].index_add_(0, t, wt.abs() * (x[t].abs() @ W[e].abs().T + b[e].abs()))
         if g is None:
             continue
