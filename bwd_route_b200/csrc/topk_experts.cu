@@ -627,9 +627,11 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinArgs A, int LPT) {
 }
 
 // ---------------------------------------------------------------- dW and db
-// Warps 0-7 scale the rows of g and drain the sums, 8-11 gather, 12 issues the MMAs.
-constexpr int kWThreads = 416;
-constexpr int kWGather0 = 8, kWMmaWarp = 12;
+// Warps 0-7 scale the rows of g and drain the sums, 8-11 gather, 12 issues the MMAs, 13
+// looks pairs up.
+constexpr int kWThreads = 448;
+constexpr int kWGather0 = 8, kWMmaWarp = 12, kWLookWarp = 13;
+constexpr int kMaxPieces = kMaxE + kWUnits;
 
 struct WCfg {
     static constexpr int KT = 32;              // pairs per stage
@@ -638,16 +640,23 @@ struct WCfg {
     static constexpr int STAGE = 2 * OP;       // g then x: 32 KiB
     static constexpr int STAGES = 6;
     static constexpr int STG = 8 * 32 * 64;    // staging: 32 rows x 64 bytes a warp
+    static constexpr int LOOK = 128;           // pairs looked up at a time
+    static constexpr int LOOKS = 3;            // blocks of them on the way
+    static constexpr int STEPS = LOOK / KT;    // stages of a block
 };
 
 struct __align__(8) WCtl {
     uint64_t raw[WCfg::STAGES], full[WCfg::STAGES], empty[WCfg::STAGES];
+    uint64_t lfull[WCfg::LOOKS], lempty[WCfg::LOOKS];
     uint64_t tfull, tempty;
     uint32_t tmem_base;
     int abort;
     int off[kMaxE + 1];
     int pstart[kMaxE + 1];  // first piece of each expert
     int sstart[kMaxE + 1];  // first slot of each expert (experts of two pieces or more)
+    uint16_t order[kMaxPieces + 4];  // pieces, most pairs first
+    int token[WCfg::LOOKS][WCfg::LOOK];    // -1 past the piece's end
+    float weight[WCfg::LOOKS][WCfg::LOOK];
     float db[8][32][8];
 };
 constexpr int kWSmem = 1024 + WCfg::STAGES * WCfg::STAGE + WCfg::STG + static_cast<int>(sizeof(WCtl));
@@ -698,6 +707,10 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
             mbar_init(&ctl->full[s], 8);   // the scaling warps
             mbar_init(&ctl->empty[s], 1);  // tcgen05.commit
         }
+        for (int s = 0; s < C::LOOKS; ++s) {
+            mbar_init(&ctl->lfull[s], 32);      // the looking lanes
+            mbar_init(&ctl->lempty[s], 8 + 4);  // scaling and gather warps
+        }
         mbar_init(&ctl->tfull, 1);
         mbar_init(&ctl->tempty, 8);
         ctl->abort = 0;
@@ -711,16 +724,38 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
     for (int e = threadIdx.x; e <= A.E; e += kWThreads) ctl->off[e] = A.offsets[e];
     __syncthreads();
     if (warp == 0) piece_starts(ctl, A.E, A.P, A.extra);
+    __syncthreads();
+    const int npieces = ctl->pstart[A.E];  // at most E + extra
+    // The pieces by size, largest first: the blocks take units in turns that run back and forth, so
+    // that a large unit is followed by a small one. The stages hold the sizes meanwhile.
+    int* sizes = reinterpret_cast<int*>(smem);
+    for (int i = threadIdx.x; i < npieces; i += kWThreads) {
+        const int e = span_of(ctl->pstart, A.E, i), n = ctl->off[e + 1] - ctl->off[e], q = ctl->pstart[e + 1] - ctl->pstart[e];
+        sizes[i] = (n + q - 1) / q;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < npieces; i += kWThreads) {
+        const int mine = sizes[i];
+        int rank = 0;
+        for (int o = 0; o < npieces; ++o) rank += (sizes[o] > mine || (sizes[o] == mine && o < i)) ? 1 : 0;
+        ctl->order[rank] = static_cast<uint16_t>(i);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     volatile int* abort = &ctl->abort;
     const int nt = (H + kWTile - 1) / kWTile, tiles = nt * nt;
-    const int nunits = ctl->pstart[A.E] * tiles;
+    const int nunits = npieces * tiles;
+    // the block's unit of a turn, -1 after the last
+    auto unit_number = [&](int turn) {
+        const int g = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+        const int64_t u = static_cast<int64_t>(turn) * g + ((turn & 1) ? g - 1 - b : b);
+        return u < nunits ? static_cast<int>(u) : -1;
+    };
     auto unit_of = [&](int u) {
         Unit r;
-        const int piece = u / tiles, tile = u - piece * tiles;
+        const int piece = ctl->order[u / tiles], tile = u % tiles;
         r.e = span_of(ctl->pstart, A.E, piece);
         r.pieces = ctl->pstart[r.e + 1] - ctl->pstart[r.e];
         r.piece = piece - ctl->pstart[r.e];
@@ -732,43 +767,87 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         return r;
     };
 
-    if (warp >= kWGather0 && warp < kWGather0 + 4) {
+    if (warp == kWLookWarp) {
+        // ---------------- lookup: tokens and weights of the pairs, up to three blocks ahead of the rows;
+        // a block's pairs are read two blocks ahead of its tokens' entry, its weights one
+        constexpr int N = C::LOOK / 32;
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int turn = 0, u; ok && (u = unit_number(turn)) >= 0; ++turn) {
+            const Unit r = unit_of(u);
+            int p0[N], p1[N];
+            float w0[N];
+            auto pairs = [&](int at, int (&p)[N]) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) p[i] = at + 32 * i + lane < r.hi ? A.perm[at + 32 * i + lane] : -1;
+            };
+            auto weights = [&](const int (&p)[N], float (&w)[N]) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) w[i] = p[i] >= 0 ? A.weights[p[i]] : 0.0f;
+            };
+            pairs(r.lo, p0);
+            pairs(r.lo + C::LOOK, p1);
+            weights(p0, w0);
+            for (int at = r.lo; at < r.hi; at += C::LOOK) {
+                int p2[N];
+                float w1[N];
+                pairs(at + 2 * C::LOOK, p2);
+                weights(p1, w1);
+                if (!(ok = mbar_wait(&ctl->lempty[slot], phase ^ 1, abort, A.flags))) break;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    ctl->token[slot][32 * i + lane] = p0[i] < 0 ? -1 : A.by_k(p0[i]);
+                    ctl->weight[slot][32 * i + lane] = w0[i];
+                    p0[i] = p1[i];
+                    p1[i] = p2[i];
+                    w0[i] = w1[i];
+                }
+                mbar_arrive(&ctl->lfull[slot]);
+                if (++slot == C::LOOKS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp >= kWGather0 && warp < kWGather0 + 4) {
         // ---------------- gather: rows of g and x as they are, MN-major; a warp moves a row of 256
         // columns at a time; rows past the piece's end are zeros
         const T* g = static_cast<const T*>(A.g);
         const T* x = static_cast<const T*>(A.x);
         const int w4 = warp - kWGather0;
-        int stage = 0;
-        uint32_t phase = 0;
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, lphase = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
+        for (int turn = 0, u; ok && (u = unit_number(turn)) >= 0; ++turn) {
             const Unit r = unit_of(u);
             const bool on_g = lane * 8 < min(kWTile, H - r.o0), on_x = lane * 8 < min(kWTile, H - r.i0);
-            // this warp's 8 rows of a stage are w4, w4 + 4, ...; lane i < 8 looks row i up, two stages ahead
-            auto look = [&](int p0) {
-                const int i = p0 + w4 + 4 * (lane & 7);
-                return i < r.hi ? A.perm[i] : -1;
-            };
-            int pair = look(r.lo), npair = look(r.lo + C::KT);
-            for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
-                const int tok = pair < 0 ? -1 : A.by_k(pair);
-                pair = npair;
-                npair = look(p0 + 2 * C::KT);
-                if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
-                const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
+            for (int at = r.lo; ok && at < r.hi; at += C::LOOK) {
+                if (!(ok = mbar_wait(&ctl->lfull[slot], lphase, abort, A.flags))) break;
+                const int steps = min(C::STEPS, (r.hi - at + C::KT - 1) / C::KT);
+                for (int st = 0; st < steps; ++st) {
+                    if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
+                    const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = w4 + 4 * i;
-                    const int tr = __shfl_sync(kFull, tok, i);
-                    const uint32_t at = base + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
-                    const int64_t src = static_cast<int64_t>(tr < 0 ? 0 : tr) * H + lane * 8;
-                    if (on_g) cp_async_16(at, g + src + r.o0, tr < 0 ? 0u : 16u);
-                    if (on_x) cp_async_16(at + C::OP, x + src + r.i0, tr < 0 ? 0u : 16u);
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = w4 + 4 * i;
+                        const int tr = ctl->token[slot][st * C::KT + row];
+                        const uint32_t to = base + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+                        const int64_t src = static_cast<int64_t>(tr < 0 ? 0 : tr) * H + lane * 8;
+                        if (on_g) cp_async_16(to, g + src + r.o0, tr < 0 ? 0u : 16u);
+                        if (on_x) cp_async_16(to + C::OP, x + src + r.i0, tr < 0 ? 0u : 16u);
+                    }
+                    cp_async_arrive_noinc(&ctl->raw[stage]);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
-                cp_async_arrive_noinc(&ctl->raw[stage]);
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->lempty[slot]);
+                if (++slot == C::LOOKS) {
+                    slot = 0;
+                    lphase ^= 1;
                 }
             }
         }
@@ -778,7 +857,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < nunits && ok; u += gridDim.x) {
+            for (int turn = 0, u; ok && (u = unit_number(turn)) >= 0; ++turn) {
                 const Unit r = unit_of(u);
                 const int halves = (min(kWTile, H - r.o0) + 127) / 128;
                 const uint32_t idesc = idesc_f16<T>(128, min(kWTile, H - r.i0), 1, 1);
@@ -811,54 +890,57 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         // 32 (w % 4) + lane of each half, columns of half w / 4
         const int q = warp & 3, ch = warp >> 2;
         const uint32_t my = smem_u32(stg + warp * 32 * 64);
-        int stage = 0;
-        uint32_t phase = 0, acc_phase = 0;
+        int stage = 0, slot = 0;
+        uint32_t phase = 0, lphase = 0, acc_phase = 0;
         bool ok = true;
         T* dW = static_cast<T*>(A.dW);
-        for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
+        for (int turn = 0, u; (u = unit_number(turn)) >= 0; ++turn) {
             const Unit r = unit_of(u);
             const int rows = min(kWTile, H - r.o0), cols = min(kWTile, H - r.i0);
             const bool on = lane * 8 < rows;
             float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            // weights of a stage's rows warp, warp + 8, ...: lane i < 4 looks row i up; the pair's number
-            // two stages ahead, its weight one
-            auto pair_at = [&](int p0) {
-                const int i = p0 + warp + 8 * (lane & 3);
-                return i < r.hi ? A.perm[i] : -1;
-            };
-            auto weight_of = [&](int p) { return p >= 0 ? A.weights[p] : 0.0f; };
-            float wt = weight_of(pair_at(r.lo));
-            int np = pair_at(r.lo + C::KT);
-            for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
-                const float nwt = weight_of(np);
-                np = pair_at(p0 + 2 * C::KT);
-                if (!(ok = mbar_wait(&ctl->raw[stage], phase, abort, A.flags))) break;
-                const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = warp + 8 * i;
-                    const float wr = __shfl_sync(kFull, wt, i);
-                    const uint32_t at = base + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+            for (int at = r.lo; ok && at < r.hi; at += C::LOOK) {
+                if (!(ok = mbar_wait(&ctl->lfull[slot], lphase, abort, A.flags))) break;
+                const int steps = min(C::STEPS, (r.hi - at + C::KT - 1) / C::KT);
+                for (int st = 0; st < steps; ++st) {
+                    if (!(ok = mbar_wait(&ctl->raw[stage], phase, abort, A.flags))) break;
+                    const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
                     if (on) {
-                        const uint4 raw = ld_shared_u4(at);
-                        const T* v = reinterpret_cast<const T*>(&raw);
-                        float s[8];
+                        uint4 raw[4];
+                        float wr[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            s[j] = wr * to_f(v[j]);
-                            db[j] += s[j];
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = warp + 8 * i;
+                            wr[i] = ctl->weight[slot][st * C::KT + row];
+                            raw[i] = ld_shared_u4(base + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
                         }
-                        st_shared_u4(at, pack8<T>(s));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = warp + 8 * i;
+                            const T* v = reinterpret_cast<const T*>(&raw[i]);
+                            float s[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                s[j] = wr[i] * to_f(v[j]);
+                                db[j] += s[j];
+                            }
+                            st_shared_u4(base + row * 128 + (((lane & 7) ^ (row & 7)) << 4), pack8<T>(s));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->full[stage]);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
                     }
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->full[stage]);
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+                if (lane == 0) mbar_arrive(&ctl->lempty[slot]);
+                if (++slot == C::LOOKS) {
+                    slot = 0;
+                    lphase ^= 1;
                 }
-                wt = nwt;
             }
             if (!ok) break;
             if (A.db && r.i0 == 0) {
