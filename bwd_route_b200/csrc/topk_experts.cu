@@ -248,7 +248,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
         const T* src = static_cast<const T*>(A.src);
         const int ptid = threadIdx.x - kPProducer0;
         const int prow = ptid >> 3, pg = ptid & 7;
-        int tok[8], nxt[8];
+        int nxt[8];
+        const T* row[8];  // this lane's 16 bytes of the first chunk of its rows
+        unsigned there = 0;
         // the pairs of a tile's rows; their tokens are worked out a tile later, when the loads are there
         auto load_pairs = [&](int tile, int (&t)[8]) {
             int e, row0, nrows;
@@ -260,11 +262,18 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
             }
         };
         auto to_tokens = [&](const int (&pair)[8]) {
+            there = 0;
 #pragma unroll
-            for (int it = 0; it < 8; ++it) tok[it] = pair[it] < 0 ? -1 : A.by_k(pair[it]);
+            for (int it = 0; it < 8; ++it) {
+                row[it] = src + static_cast<int64_t>(pair[it] < 0 ? 0 : A.by_k(pair[it])) * H + pg * 8;
+                there |= pair[it] < 0 ? 0u : 1u << it;
+            }
         };
-        if (static_cast<int>(blockIdx.x) < ntiles) load_pairs(blockIdx.x, nxt);
-        to_tokens(nxt);
+        if (static_cast<int>(blockIdx.x) < ntiles) {
+            load_pairs(blockIdx.x, nxt);
+            to_tokens(nxt);
+        }
+        const uint32_t to = smem_u32(aring) + prow * 128 + ((pg ^ (prow & 7)) << 4);  // rows 16 apart swizzle alike
         int sa = 0;
         uint32_t pa = 0;
         bool ok = true;
@@ -272,14 +281,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
             if (tile + static_cast<int>(gridDim.x) < ntiles) load_pairs(tile + gridDim.x, nxt);
             for (int kc = 0; kc < KCH; ++kc) {
                 if (!(ok = mbar_wait(&ctl->aempty[sa], pa ^ 1, abort, A.flags))) break;
-                const uint32_t a_u32 = smem_u32(aring + sa * C::A_BYTES);
+                const uint32_t a_u32 = to + sa * C::A_BYTES;
 #pragma unroll
-                for (int it = 0; it < 8; ++it) {
-                    const int r = it * 16 + prow;
-                    const int t = tok[it];
-                    cp_async_16_l2_256(a_u32 + r * 128 + ((pg ^ (r & 7)) << 4),
-                                       src + static_cast<int64_t>(t < 0 ? 0 : t) * H + kc * 64 + pg * 8, t < 0 ? 0u : 16u);
-                }
+                for (int it = 0; it < 8; ++it)
+                    cp_async_16_l2_256(a_u32 + it * 16 * 128, row[it] + kc * 64, (there >> it) & 1u ? 16u : 0u);
                 cp_async_arrive_noinc(&ctl->afull[sa]);
                 if (++sa == C::A_STAGES) {
                     sa = 0;
@@ -645,7 +650,9 @@ struct WCfg {
     static constexpr int STEPS = LOOK / KT;    // stages of a block
 };
 
-struct __align__(8) WCtl {
+struct __align__(16) WCtl {
+    int64_t row[WCfg::LOOKS][WCfg::LOOK];  // first element of the pair's token
+    float weight[WCfg::LOOKS][WCfg::LOOK];
     uint64_t raw[WCfg::STAGES], full[WCfg::STAGES], empty[WCfg::STAGES];
     uint64_t lfull[WCfg::LOOKS], lempty[WCfg::LOOKS];
     uint64_t tfull, tempty;
@@ -655,8 +662,6 @@ struct __align__(8) WCtl {
     int pstart[kMaxE + 1];  // first piece of each expert
     int sstart[kMaxE + 1];  // first slot of each expert (experts of two pieces or more)
     uint16_t order[kMaxPieces + 4];  // pieces, most pairs first
-    int token[WCfg::LOOKS][WCfg::LOOK];    // -1 past the piece's end
-    float weight[WCfg::LOOKS][WCfg::LOOK];
     float db[8][32][8];
 };
 constexpr int kWSmem = 1024 + WCfg::STAGES * WCfg::STAGE + WCfg::STG + static_cast<int>(sizeof(WCtl));
@@ -704,7 +709,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&ctl->raw[s], 128);  // the gather threads' copies
-            mbar_init(&ctl->full[s], 8);   // the scaling warps
+            mbar_init(&ctl->full[s], 4);   // the four warps that scale it
             mbar_init(&ctl->empty[s], 1);  // tcgen05.commit
         }
         for (int s = 0; s < C::LOOKS; ++s) {
@@ -797,7 +802,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                 if (!(ok = mbar_wait(&ctl->lempty[slot], phase ^ 1, abort, A.flags))) break;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    ctl->token[slot][32 * i + lane] = p0[i] < 0 ? -1 : A.by_k(p0[i]);
+                    ctl->row[slot][32 * i + lane] = p0[i] < 0 ? 0 : static_cast<int64_t>(A.by_k(p0[i])) * H;
                     ctl->weight[slot][32 * i + lane] = w0[i];
                     p0[i] = p1[i];
                     p1[i] = p2[i];
@@ -819,23 +824,33 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         int stage = 0, slot = 0;
         uint32_t phase = 0, lphase = 0;
         bool ok = true;
+        // a warp has rows 8 w4 .. 8 w4 + 7 of a stage: row i of them swizzles by i
+        uint32_t to[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            to[i] = smem_u32(smem) + (lane >> 3) * C::GROUP + (8 * w4 + i) * 128 + (((lane & 7) ^ i) << 4);
         for (int turn = 0, u; ok && (u = unit_number(turn)) >= 0; ++turn) {
             const Unit r = unit_of(u);
             const bool on_g = lane * 8 < min(kWTile, H - r.o0), on_x = lane * 8 < min(kWTile, H - r.i0);
+            const T* gl = g + r.o0 + (on_g ? lane * 8 : 0);
+            const T* xl = x + r.i0 + (on_x ? lane * 8 : 0);
             for (int at = r.lo; ok && at < r.hi; at += C::LOOK) {
                 if (!(ok = mbar_wait(&ctl->lfull[slot], lphase, abort, A.flags))) break;
                 const int steps = min(C::STEPS, (r.hi - at + C::KT - 1) / C::KT);
                 for (int st = 0; st < steps; ++st) {
+                    longlong2 rows[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        rows[i] = *reinterpret_cast<const longlong2*>(&ctl->row[slot][st * C::KT + 8 * w4 + 2 * i]);
+                    const int left = r.hi - at - st * C::KT - 8 * w4;  // rows of the warp that are pairs
                     if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
-                    const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
+                    const uint32_t base = stage * C::STAGE;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int row = w4 + 4 * i;
-                        const int tr = ctl->token[slot][st * C::KT + row];
-                        const uint32_t to = base + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
-                        const int64_t src = static_cast<int64_t>(tr < 0 ? 0 : tr) * H + lane * 8;
-                        if (on_g) cp_async_16(to, g + src + r.o0, tr < 0 ? 0u : 16u);
-                        if (on_x) cp_async_16(to + C::OP, x + src + r.i0, tr < 0 ? 0u : 16u);
+                        const int64_t row = (i & 1) ? rows[i / 2].y : rows[i / 2].x;
+                        const uint32_t bytes = i < left ? 16u : 0u;
+                        if (on_g) cp_async_16(to[i] + base, gl + row, bytes);
+                        if (on_x) cp_async_16(to[i] + base + C::OP, xl + row, bytes);
                     }
                     cp_async_arrive_noinc(&ctl->raw[stage]);
                     if (++stage == C::STAGES) {
@@ -894,42 +909,55 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         uint32_t phase = 0, lphase = 0, acc_phase = 0;
         bool ok = true;
         T* dW = static_cast<T*>(A.dW);
+        // warps 0-3 scale the even stages, 4-7 the odd ones (there is an even number), so that one stage's
+        // latency hides behind the other's; rows 8 q .. 8 q + 7, row i of them swizzled by i
+        static_assert(C::STAGES % 2 == 0, "a stage has the same warps every time");
+        uint32_t to[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            to[i] = smem_u32(smem) + (lane >> 3) * C::GROUP + (8 * q + i) * 128 + (((lane & 7) ^ i) << 4);
         for (int turn = 0, u; (u = unit_number(turn)) >= 0; ++turn) {
             const Unit r = unit_of(u);
             const int rows = min(kWTile, H - r.o0), cols = min(kWTile, H - r.i0);
             const bool on = lane * 8 < rows;
+            const bool add = A.db && r.i0 == 0;
             float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             for (int at = r.lo; ok && at < r.hi; at += C::LOOK) {
                 if (!(ok = mbar_wait(&ctl->lfull[slot], lphase, abort, A.flags))) break;
                 const int steps = min(C::STEPS, (r.hi - at + C::KT - 1) / C::KT);
                 for (int st = 0; st < steps; ++st) {
-                    if (!(ok = mbar_wait(&ctl->raw[stage], phase, abort, A.flags))) break;
-                    const uint32_t base = smem_u32(smem + stage * C::STAGE) + (lane >> 3) * C::GROUP;
-                    if (on) {
-                        uint4 raw[4];
-                        float wr[4];
+                    if ((stage & 1) == ch) {
+                        float wr[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = warp + 8 * i;
-                            wr[i] = ctl->weight[slot][st * C::KT + row];
-                            raw[i] = ld_shared_u4(base + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 w4 = *reinterpret_cast<const float4*>(&ctl->weight[slot][st * C::KT + 8 * q + 4 * i]);
+                            wr[4 * i] = w4.x;
+                            wr[4 * i + 1] = w4.y;
+                            wr[4 * i + 2] = w4.z;
+                            wr[4 * i + 3] = w4.w;
                         }
+                        if (!(ok = mbar_wait(&ctl->raw[stage], phase, abort, A.flags))) break;
+                        const uint32_t base = stage * C::STAGE;
+                        if (on) {
+                            uint4 raw[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = warp + 8 * i;
-                            const T* v = reinterpret_cast<const T*>(&raw[i]);
-                            float s[8];
+                            for (int i = 0; i < 8; ++i) raw[i] = ld_shared_u4(to[i] + base);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                s[j] = wr[i] * to_f(v[j]);
-                                db[j] += s[j];
+                            for (int i = 0; i < 8; ++i) {
+                                const T* v = reinterpret_cast<const T*>(&raw[i]);
+                                float s[8];
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) s[j] = wr[i] * to_f(v[j]);
+                                if (add)
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) db[j] += s[j];
+                                st_shared_u4(to[i] + base, pack8<T>(s));
                             }
-                            st_shared_u4(base + row * 128 + (((lane & 7) ^ (row & 7)) << 4), pack8<T>(s));
                         }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->full[stage]);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->full[stage]);
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -943,7 +971,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                 }
             }
             if (!ok) break;
-            if (A.db && r.i0 == 0) {
+            if (add) {
                 // the eight warps' sums, in order
                 asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll
