@@ -555,7 +555,7 @@ struct JoinArgs {
 // LPT lanes per token, 8 columns each at a time; U tokens per turn, so that enough loads
 // are on the way; KM: an upper bound of K. DW: the backward (d_weights may be NULL).
 template <typename T, int KM, int U, bool DW>
-__global__ void __launch_bounds__(256) join_kernel(const JoinArgs A, int LPT) {
+__global__ void __launch_bounds__(256, KM <= 2 ? 4 : KM <= 4 ? 3 : 2) join_kernel(const JoinArgs A, int LPT) {
     griddep_wait();  // every global access below comes after the previous grid
     const int lane = threadIdx.x & 31, sub = lane % LPT, K = A.K, H = A.H, per_warp = 32 / LPT;
     const int64_t P = A.T * K;
@@ -1169,7 +1169,7 @@ cudaError_t join_launch(const JoinArgs& a, int sms, cudaStream_t s) {
         const int64_t tokens = 8 * (32 / lpt) * u, want = (a.T + tokens - 1) / tokens, cap = static_cast<int64_t>(sms) * 8;
         return launch_pdl(kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s, a, lpt);
     };
-    if (a.K <= 2) return go(join_kernel<T, 2, 2, DW>, 2);
+    if (a.K <= 2) return DW ? go(join_kernel<T, 2, 1, DW>, 1) : go(join_kernel<T, 2, 2, DW>, 2);
     if (a.K <= 4) return go(join_kernel<T, 4, 1, DW>, 1);
     if (a.K <= 8) return go(join_kernel<T, 8, 1, DW>, 1);
     return go(join_kernel<T, 16, 1, DW>, 1);
