@@ -1,6 +1,7 @@
 // topk.h -- host-side declarations shared by the files of the top-k block.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -14,6 +15,10 @@ inline size_t dtype_bytes(moe_dtype_t d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
 
 // SMs of the current device.
 cudaError_t device_sms(int* out);
+
+// The dynamic shared-memory limit of a kernel, set once per device: `done` is a bit per
+// device, a static of the caller's.
+cudaError_t set_smem_once(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // Workspace of the router: the reserved head, then per-block counts and bases.
 size_t topk_route_ws_bytes(int64_t T, int E);

@@ -28,6 +28,18 @@ cudaError_t device_sms(int* out) {
     return cudaSuccess;
 }
 
+cudaError_t set_smem_once(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const uint64_t bit = uint64_t{1} << dev;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 }  // namespace moe
 
 extern "C" int32_t moe_topk_abi_version(void) { return MOE_TOPK_ABI_VERSION; }

@@ -28,6 +28,7 @@
 //     pairs.
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "checks.h"
 #include "common.cuh"
@@ -1119,16 +1120,45 @@ __global__ void __launch_bounds__(256) wgrad_sum_kernel(const WgradArgs A) {
 }
 
 // ---------------------------------------------------------------- launches
+// The tensor map of a weight array depends on the arguments alone; the last ones are kept,
+// so a layer's calls encode its map once.
+struct MapKey {
+    const void* W;
+    moe_dtype_t dtype;
+    uint64_t rows, cols;
+    uint32_t box_rows;
+    bool operator==(const MapKey& o) const {
+        return W == o.W && dtype == o.dtype && rows == o.rows && cols == o.cols && box_rows == o.box_rows;
+    }
+};
+constexpr int kMaps = 16;
+MapKey g_map_key[kMaps];
+CUtensorMap g_map[kMaps];
+int g_maps = 0, g_map_next = 0;
+std::mutex g_map_mu;
+
 bool weight_map(CUtensorMap* map, const void* W, moe_dtype_t dtype, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+    const MapKey key{W, dtype, rows, cols, box_rows};
+    std::lock_guard<std::mutex> lock(g_map_mu);
+    for (int i = 0; i < g_maps; ++i)
+        if (g_map_key[i] == key) {
+            *map = g_map[i];
+            return true;
+        }
     EncodeTiledFn enc = get_encode_tiled();
     if (!enc) return false;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols * 2};
     const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return enc(map, dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-               const_cast<void*>(W), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    if (enc(map, dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(W), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    const int at = g_maps < kMaps ? g_maps++ : g_map_next++ % kMaps;
+    g_map_key[at] = key;
+    g_map[at] = *map;
+    return true;
 }
 
 template <typename T, int BN, bool DX>
@@ -1137,7 +1167,8 @@ cudaError_t pair_launch(const void* W, moe_dtype_t dtype, const PairArgs& a, int
     CUtensorMap map;
     if (!weight_map(&map, W, dtype, static_cast<uint64_t>(a.E) * a.H, a.H, DX ? 64 : BN)) return cudaErrorInvalidValue;
     auto kernel = a.K == 1 ? pair_kernel<T, BN, DX, true> : pair_kernel<T, BN, DX, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    static std::atomic<uint64_t> ready[2];
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES, ready[a.K == 1 ? 1 : 0]);
     if (e != cudaSuccess) return e;
     const int nt = (a.H + BN - 1) / BN;
     *parts = nt * C::HALVES;
@@ -1196,7 +1227,8 @@ cudaError_t fwd_type(const void* W, moe_dtype_t dtype, const PairArgs& a, int64_
 
 template <typename T>
 cudaError_t wgrad_launch(const WgradArgs& a, int sms, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
+    static std::atomic<uint64_t> ready;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(wgrad_kernel<T>), kWSmem, ready);
     if (e != cudaSuccess) return e;
     const int64_t hit = a.P < a.E ? a.P : a.E;
     const int64_t units = (hit + a.extra) * wgrad_tiles(a.H);

@@ -986,7 +986,8 @@ int small_smem(const RouteArgs& a, int warp_area) {
 template <typename T, int VPL, int MODE>
 cudaError_t route_small(const RouteArgs& a, int smem, cudaStream_t s) {
     auto kernel = topk_route_small_kernel<T, 32, VPL, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    static std::atomic<uint64_t> ready;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), 200 * 1024, ready);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(1), dim3(kSmallThreads), smem, s, static_cast<const T*>(a.logits), a.ld,
                       static_cast<int>(a.T), a.vec, a.bias, a.R, a.out.expert_idx, a.weights, a.out.counts, a.out.offsets,
@@ -1010,7 +1011,8 @@ cudaError_t route_launch(const RouteArgs& a, cudaStream_t s) {
     const int nblk = static_cast<int>((a.T + tpb - 1) / tpb);
     const int smem = kMaxE * 4 + kWarps * wb;
     auto kernel = topk_route_kernel<T, LPT, VPL, MODE>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+    static std::atomic<uint64_t> ready;
+    e = set_smem_once(reinterpret_cast<const void*>(kernel), 128 * 1024, ready);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(nblk), dim3(kThreads), smem, s, static_cast<const T*>(a.logits), a.ld, a.T, tpb, a.vec,
                    a.bias, R, a.out.expert_idx, a.weights, a.blk_counts);

@@ -324,43 +324,64 @@ def moe_top1_device_flags(ws: torch.Tensor, stream=None) -> int:
 
 
 # ---------------------------------------------------------------- top-k block
-def _arg(name: str, t: torch.Tensor | None, dev: int, dtype, *shape):
-    """Address of a dense tensor of this type and shape on device dev, or None."""
-    if t is None:
-        return None
-    if t.device.index != dev or not t.is_cuda:
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _refuse(name: str, t: torch.Tensor, dev: int, dtype, shape):
+    """What is wrong with a tensor that _arg does not take."""
+    if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
+    raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _arg(name: str, t: torch.Tensor | None, dev: int, dtype, *shape):
+    """Address of a dense tensor of this type and shape on device dev, or None."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, dev, dtype, shape)
     return t.data_ptr()
 
 
 def _rows(name: str, t: torch.Tensor):
     """(device, dtype, rows, columns, row stride) of a [T, H] tensor with dense rows
     on the current device, the one whose stream the call is enqueued on."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"{name}: expected a tensor on the current CUDA device, got {t.device}")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name}: expected a [T, H] tensor, got shape {tuple(t.shape)}")
     T, H = t.shape
-    if H > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if H > 1 and inner != 1:
         raise ValueError(f"{name}: expected rows of adjacent elements")
-    ld = t.stride(0) if T > 1 else H
-    if ld < H:
+    if T <= 1:
+        ld = H
+    elif ld < H:
         raise ValueError(f"{name}: expected rows that do not overlap")
-    return t.device.index, t.dtype, T, H, ld
+    return dev, t.dtype, T, H, ld
+
+
+def _on(stream, dev: int):
+    """Handle of the given torch stream, else of the device's current stream."""
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError(f"expected a stream of cuda:{dev}")
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _workspace(ws: torch.Tensor | None, dev: int):
     if ws is None:
         return None, 0
-    return _arg("ws", ws, dev, torch.uint8, ws.numel()), ws.numel()
+    n = ws.numel()
+    return _arg("ws", ws, dev, torch.uint8, n), n
 
 
 @dataclasses.dataclass(frozen=True)
@@ -409,7 +430,7 @@ def moe_topk_route(logits, rule: TopKRule, bias, routing: Routing, weights, ws: 
     w, n = _workspace(ws, dev)
     _check("moe_topk_route",
            lib().moe_topk_route(logits.data_ptr(), _DTYPES[dt], T, ld, rule._c, _arg("bias", bias, dev, f, E), rc,
-                                _arg("weights", weights, dev, f, T, rule.K), w, n, _stream(stream)))
+                                _arg("weights", weights, dev, f, T, rule.K), w, n, _on(stream, dev)))
 
 
 def moe_topk_route_bwd(logits, rule: TopKRule, expert_idx, d_weights, d_logits, accumulate: bool = False, stream=None):
@@ -423,7 +444,7 @@ def moe_topk_route_bwd(logits, rule: TopKRule, expert_idx, d_weights, d_logits, 
                                     _arg("expert_idx", expert_idx.view(-1), dev, torch.int32, T * rule.K),
                                     _arg("d_weights", d_weights, dev, torch.float32, T, rule.K),
                                     _arg("d_logits", d_logits, dev, dt, T, E), 1 if accumulate else 0,
-                                    _stream(stream)))
+                                    _on(stream, dev)))
 
 
 def _experts(x, W, weights):
@@ -447,7 +468,7 @@ def moe_topk_fwd(x, W, bias, routing: Routing, weights, y, ws: torch.Tensor, str
            lib().moe_topk_fwd(x.data_ptr(), _arg("W", W, dev, dt, E, H, H), _arg("bias", bias, dev, dt, E, H),
                               _DTYPES[dt], _pairs(routing, dev, T * K, E),
                               _arg("weights", weights, dev, torch.float32, T, K), T, E, K, H,
-                              _arg("y", y, dev, dt, T, H), w, n, _stream(stream)))
+                              _arg("y", y, dev, dt, T, H), w, n, _on(stream, dev)))
 
 
 def moe_topk_bwd(x, W, bias, d_out, routing: Routing, weights, d_x, dW, db, d_weights, ws: torch.Tensor, stream=None):
@@ -460,7 +481,7 @@ def moe_topk_bwd(x, W, bias, d_out, routing: Routing, weights, d_x, dW, db, d_we
                               _DTYPES[dt], _arg("d_out", d_out, dev, dt, T, H), _pairs(routing, dev, T * K, E),
                               _arg("weights", weights, dev, f, T, K), T, E, K, H, _arg("d_x", d_x, dev, dt, T, H),
                               _arg("dW", dW, dev, dt, E, H, H), _arg("db", db, dev, dt, E, H),
-                              _arg("d_weights", d_weights, dev, f, T, K), w, n, _stream(stream)))
+                              _arg("d_weights", d_weights, dev, f, T, K), w, n, _on(stream, dev)))
 
 
 def moe_layer_norm_workspace_bytes(T: int, H: int) -> int:
@@ -491,7 +512,7 @@ def moe_layer_norm_fwd(x, gamma, beta, eps: float, y, mean=None, rstd=None, stre
     _check("moe_layer_norm_fwd",
            lib().moe_layer_norm_fwd(x.data_ptr(), _DTYPES[dt], T, H, ld, _arg("gamma", gamma, dev, pd, H),
                                     _arg("beta", beta, dev, pd, H), _DTYPES[pd], eps, _arg("y", y, dev, dt, T, H),
-                                    _arg("mean", mean, dev, f, T), _arg("rstd", rstd, dev, f, T), _stream(stream)))
+                                    _arg("mean", mean, dev, f, T), _arg("rstd", rstd, dev, f, T), _on(stream, dev)))
 
 
 def moe_layer_norm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
@@ -505,4 +526,4 @@ def moe_layer_norm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=N
                                     _arg("gamma", gamma, dev, pd, H), _DTYPES[pd], _arg("mean", mean, dev, f, T),
                                     _arg("rstd", rstd, dev, f, T), _arg("dx", dx, dev, dt, T, H),
                                     _arg("dgamma", dgamma, dev, pd, H), _arg("dbeta", dbeta, dev, pd, H), w, n,
-                                    _stream(stream)))
+                                    _on(stream, dev)))
