@@ -18,6 +18,7 @@
 //     [2^14, 2^15)): half of fp32's traffic at 11 bits, finer than bf16's 8, whatever the
 //     magnitude. The backward's epilogue also takes x . (W_e^T g) from the fp32
 //     accumulators, with its warps' rows of x brought in by cp.async beside them.
+//   duo_kernel    : y and d_x for K = 2 and many tokens: see there.
 //   join_kernel   : adds the K rows of a token (and w b_e) in the order of k in fp32, one
 //     rounding; in the backward also d_w from the column parts and g . b_e.
 //   wgrad_kernel  : dW and db. The pairs are the contraction index: both operands are
@@ -171,6 +172,11 @@ struct PairCfg {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
+struct DuoWs {
+    int32_t* count;  // [E * E] counts, [E * E] places taken, [E * E + 1] starts
+    int32_t* list;   // [T]
+};
+
 struct PairArgs {
     const void* src;       // rows of tokens: x (y) or d_out (d_x)
     const void* other;     // d_x: x, for the weights' gradient (may be NULL)
@@ -185,6 +191,7 @@ struct PairArgs {
     __half* rows;          // [P][H], K > 1
     float* scale;          // [P][H / 32], K > 1
     float* dw_part;        // [parts][P], d_x with `other`
+    DuoWs duo;             // K = 2: see duo_kernel
     uint32_t* flags;
 };
 
@@ -526,6 +533,466 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                 A.dw_part[static_cast<int64_t>(nt * C::HALVES + half) * A.P + p] = dot;
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1;
+        }
+        if (DX) asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kPMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------- two experts per token
+// K = 2 with many tokens per pair of experts: the tokens are grouped by their two experts
+// (lo <= hi), so that a tile of 128 tokens has both products in tensor memory at once and
+// writes the sum itself: x is read once, no row waits for another, one rounding.
+constexpr int kDuoMaxE = 32, kDuoMaxH = 256;
+constexpr int kDuoTokens = 2048;  // tokens of a block of the two grouping kernels
+
+// Counts of the classes lo * E + hi over a block's tokens, added to count [E * E] (zeroed).
+__global__ void __launch_bounds__(256) duo_count_kernel(const int32_t* __restrict__ expert_idx, int64_t T_, int E,
+                                                        int32_t* __restrict__ count) {
+    griddep_wait();  // every global access below comes after the previous grid
+    __shared__ int hist[kDuoMaxE * kDuoMaxE];
+    const int n = E * E;
+    for (int i = threadIdx.x; i < n; i += 256) hist[i] = 0;
+    __syncthreads();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kDuoTokens;
+#pragma unroll
+    for (int j = 0; j < kDuoTokens / 256; ++j) {
+        const int64_t t = t0 + j * 256 + threadIdx.x;
+        if (t < T_) {
+            const int2 e = *reinterpret_cast<const int2*>(expert_idx + 2 * t);
+            atomicAdd(&hist[min(e.x, e.y) * E + max(e.x, e.y)], 1);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += 256)
+        if (hist[i]) atomicAdd(&count[i], hist[i]);
+}
+
+// list: the tokens by class, as 2 t + (the slot of the lower expert); start [E * E + 1]: where
+// each class begins. The order inside a class varies from run to run and changes no result:
+// a token's numbers do not depend on its row. taken [E * E] (zeroed): places given out.
+__global__ void __launch_bounds__(256)
+duo_group_kernel(const int32_t* __restrict__ expert_idx, int64_t T_, int E, const int32_t* __restrict__ count,
+                 int32_t* __restrict__ taken, int32_t* __restrict__ start, int32_t* __restrict__ list) {
+    griddep_wait();  // every global access below comes after the previous grid
+    __shared__ int hist[kDuoMaxE * kDuoMaxE], base[kDuoMaxE * kDuoMaxE];
+    __shared__ int s_warp[8];
+    const int n = E * E;
+    for (int i = threadIdx.x; i < n; i += 256) hist[i] = 0;
+    __syncthreads();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kDuoTokens;
+    constexpr int N = kDuoTokens / 256;
+    int bin[N], rank[N], code[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int64_t t = t0 + j * 256 + threadIdx.x;
+        bin[j] = -1;
+        if (t < T_) {
+            const int2 e = *reinterpret_cast<const int2*>(expert_idx + 2 * t);
+            bin[j] = min(e.x, e.y) * E + max(e.x, e.y);
+            code[j] = static_cast<int>(2 * t) + (e.x <= e.y ? 0 : 1);
+            rank[j] = atomicAdd(&hist[bin[j]], 1);
+        }
+    }
+    // exclusive sums of the counts: four neighbouring classes a thread
+    int c[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int b = threadIdx.x * 4 + i;
+        c[i] = b < n ? count[b] : 0;
+        sum += c[i];
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(kFull, incl, off);
+        if (lane >= off) incl += u;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int at = incl - sum;
+    for (int w = 0; w < warp; ++w) at += s_warp[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int b = threadIdx.x * 4 + i;
+        if (b < n) {
+            base[b] = at + (hist[b] ? atomicAdd(&taken[b], hist[b]) : 0);
+            if (blockIdx.x == 0) start[b] = at;
+        }
+        at += c[i];
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) start[n] = static_cast<int32_t>(T_);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (bin[j] >= 0) list[base[bin[j]] + rank[j]] = code[j];
+}
+
+// Warps as in pair_kernel. A tile's rows (all of H, at most 4 chunks of 64 columns) stay in
+// shared memory while both experts' weights pass by, 128 output columns at a time; the two
+// accumulators of those columns are one half of tensor memory.
+template <bool DX>
+struct DuoCfg {
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
+    static constexpr int A_STAGES = 8;  // two tiles of 256 columns
+    static constexpr int B_STAGES = DX ? 3 : 4;
+    static constexpr int RING_BYTES = A_STAGES * A_BYTES + B_STAGES * B_BYTES;
+    static constexpr int STEP_BYTES = 32 * 64;
+    static constexpr int STG_BYTES = kPEpiWarps * STEP_BYTES * (DX ? 2 : 1);
+    static constexpr int TMEM_COLS = 512;
+};
+
+struct __align__(8) DuoCtl {
+    uint64_t afull[8], aempty[8], bfull[4], bempty[4];
+    uint64_t tfull[2], tempty[2];
+    uint32_t tmem_base;
+    int abort;
+    int start[kDuoMaxE * kDuoMaxE + 1];
+    int tstart[kDuoMaxE * kDuoMaxE + 1];
+};
+template <bool DX>
+constexpr int duo_smem() { return 1024 + DuoCfg<DX>::RING_BYTES + DuoCfg<DX>::STG_BYTES + static_cast<int>(sizeof(DuoCtl)); }
+static_assert(duo_smem<false>() <= 227 * 1024 && duo_smem<true>() <= 227 * 1024, "shared memory");
+
+struct DuoArgs {
+    const void* src;       // rows of tokens: x (y) or d_out (d_x)
+    const void* other;     // d_x: x, for the weights' gradient (may be NULL)
+    const void* bias;      // y: may be NULL
+    const float* weights;  // [T][2]
+    const int32_t* start;  // [E * E + 1]
+    const int32_t* list;   // [T]
+    int E, H;
+    int64_t P;
+    void* out;             // [T][H]; d_x: may be NULL
+    float* dw_part;        // [2][P], d_x with `other`
+    uint32_t* flags;
+};
+
+template <typename T, bool DX>
+__global__ void __launch_bounds__(kPairThreads, 1)
+duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
+    using C = DuoCfg<DX>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* aring = smem;
+    uint8_t* bring = smem + C::A_STAGES * C::A_BYTES;
+    uint8_t* stg = smem + C::RING_BYTES;
+    DuoCtl* ctl = reinterpret_cast<DuoCtl*>(smem + C::RING_BYTES + C::STG_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = A.H, KCH = H / 64, NS = (H + 127) / 128, n = A.E * A.E;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::A_STAGES; ++s) {
+            mbar_init(&ctl->afull[s], 128);  // 128 gather threads
+            mbar_init(&ctl->aempty[s], 1);   // tcgen05.commit
+        }
+        for (int s = 0; s < C::B_STAGES; ++s) {
+            mbar_init(&ctl->bfull[s], 1);    // arrive.expect_tx + TMA bytes
+            mbar_init(&ctl->bempty[s], 1);   // tcgen05.commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl->tfull[b], 1);
+            mbar_init(&ctl->tempty[b], kPEpiWarps);
+        }
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kPLoadWarp && lane == 0) tma_prefetch_desc(&tm_w);
+    if (warp == kPMmaWarp) {
+        tmem_alloc(&ctl->tmem_base, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    griddep_wait();  // the prologue above overlaps the previous kernel; global memory from here on
+    for (int i = threadIdx.x; i <= n; i += kPairThreads) ctl->start[i] = A.start[i];
+    __syncthreads();
+    if (warp == 0) warp_starts(ctl->tstart, n, [&](int i) { return (ctl->start[i + 1] - ctl->start[i] + 127) / 128; });
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    const int ntiles = ctl->tstart[n];
+    volatile int* abort = &ctl->abort;
+    auto tile_rows = [&](int tile, int& cls, int& row0, int& nrows) {
+        cls = span_of(ctl->tstart, n, tile);
+        row0 = ctl->start[cls] + (tile - ctl->tstart[cls]) * 128;
+        nrows = min(128, ctl->start[cls + 1] - row0);
+    };
+
+    if (warp >= kPProducer0 / 32 && warp < kPProducer0 / 32 + 4) {
+        // ---------------- row gather
+        const T* src = static_cast<const T*>(A.src);
+        const int ptid = threadIdx.x - kPProducer0;
+        const int prow = ptid >> 3, pg = ptid & 7;
+        int nxt[8];
+        const T* row[8];
+        unsigned there = 0;
+        auto load_codes = [&](int tile, int (&c)[8]) {
+            int cls, row0, nrows;
+            tile_rows(tile, cls, row0, nrows);
+#pragma unroll
+            for (int it = 0; it < 8; ++it) c[it] = it * 16 + prow < nrows ? A.list[row0 + it * 16 + prow] : -1;
+        };
+        auto to_rows = [&](const int (&c)[8]) {
+            there = 0;
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                row[it] = src + static_cast<int64_t>(c[it] < 0 ? 0 : c[it] >> 1) * H + pg * 8;
+                there |= c[it] < 0 ? 0u : 1u << it;
+            }
+        };
+        if (static_cast<int>(blockIdx.x) < ntiles) {
+            load_codes(blockIdx.x, nxt);
+            to_rows(nxt);
+        }
+        const uint32_t to = smem_u32(aring) + prow * 128 + ((pg ^ (prow & 7)) << 4);  // rows 16 apart swizzle alike
+        int sa = 0;
+        uint32_t pa = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+            if (tile + static_cast<int>(gridDim.x) < ntiles) load_codes(tile + gridDim.x, nxt);
+            for (int kc = 0; kc < KCH; ++kc) {
+                if (!(ok = mbar_wait(&ctl->aempty[sa], pa ^ 1, abort, A.flags))) break;
+                const uint32_t a_u32 = to + sa * C::A_BYTES;
+#pragma unroll
+                for (int it = 0; it < 8; ++it)
+                    cp_async_16_l2_256(a_u32 + it * 16 * 128, row[it] + kc * 64, (there >> it) & 1u ? 16u : 0u);
+                cp_async_arrive_noinc(&ctl->afull[sa]);
+                if (++sa == C::A_STAGES) {
+                    sa = 0;
+                    pa ^= 1;
+                }
+            }
+            to_rows(nxt);
+        }
+    } else if (warp == kPLoadWarp) {
+        // ---------------- weight loader: columns, experts, chunks in the MMAs' order
+        if (lane == 0) {
+            int sb = 0;
+            uint32_t pb = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+                int cls, row0, nrows;
+                tile_rows(tile, cls, row0, nrows);
+                const int e2[2] = {cls / A.E, cls % A.E};
+                for (int step = 0; step < NS * 2 && ok; ++step) {
+                    const int n0 = (step >> 1) * 128, e = e2[step & 1];
+                    const int ng = min(128, H - n0) / 64;
+                    for (int kc = 0; kc < KCH; ++kc) {
+                        if (!(ok = mbar_wait(&ctl->bempty[sb], pb ^ 1, abort, A.flags))) break;
+                        if (DX) {
+                            mbar_arrive_expect_tx(&ctl->bfull[sb], ng * 64 * 128);
+                            for (int g = 0; g < ng; ++g)
+                                tma_load_2d(bring + sb * C::B_BYTES + g * 64 * 128, &tm_w, n0 + g * 64, e * H + kc * 64,
+                                            &ctl->bfull[sb]);
+                        } else {
+                            mbar_arrive_expect_tx(&ctl->bfull[sb], C::B_BYTES);
+                            tma_load_2d(bring + sb * C::B_BYTES, &tm_w, kc * 64, e * H + n0, &ctl->bfull[sb]);
+                        }
+                        if (++sb == C::B_STAGES) {
+                            sb = 0;
+                            pb ^= 1;
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kPMmaWarp) {
+        // ---------------- MMA issuer (one thread): accumulators of expert s, columns step, at
+        // 256 buf + 128 s
+        if (lane == 0) {
+            int sa = 0, sb = 0;
+            uint32_t pa = 0, pb = 0;
+            int buf = 0;
+            uint32_t buf_phase = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+                for (int ns = 0; ns < NS && ok; ++ns) {
+                    if (!(ok = mbar_wait(&ctl->tempty[buf], buf_phase ^ 1, abort, A.flags))) break;
+                    tc_fence_after();
+                    const uint32_t idesc = idesc_f16<T>(128, min(128, H - ns * 128), 0, DX ? 1 : 0);
+                    for (int s = 0; s < 2 && ok; ++s) {
+                        const uint32_t d = tmem + static_cast<uint32_t>(buf * 256 + s * 128);
+                        for (int kc = 0; kc < KCH; ++kc) {
+                            const int a = (sa + kc) % C::A_STAGES;
+                            if (ns == 0 && s == 0) {
+                                const uint32_t ph = pa ^ (sa + kc >= C::A_STAGES ? 1u : 0u);
+                                if (!(ok = mbar_wait(&ctl->afull[a], ph, abort, A.flags))) break;
+                            }
+                            if (!(ok = mbar_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
+                            fence_proxy_async_smem();
+                            tc_fence_after();
+                            const uint32_t a_addr = smem_u32(aring + a * C::A_BYTES);
+                            const uint32_t b_addr = smem_u32(bring + sb * C::B_BYTES);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks) {
+                                const uint64_t bdesc = DX ? mn_desc(b_addr + ks * 2048, 64 * 128) : sw128_desc(b_addr + ks * 32, 16, 1024);
+                                mma_f16(d, sw128_desc(a_addr + ks * 32, 16, 1024), bdesc, idesc, (kc | ks) != 0 ? 1u : 0u);
+                            }
+                            mma_commit(&ctl->bempty[sb]);
+                            if (ns == NS - 1 && s == 1) mma_commit(&ctl->aempty[a]);
+                            if (++sb == C::B_STAGES) {
+                                sb = 0;
+                                pb ^= 1;
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(&ctl->tfull[buf]);
+                    buf ^= 1;
+                    if (buf == 0) buf_phase ^= 1;
+                }
+                sa += KCH;
+                if (sa >= C::A_STAGES) {
+                    sa -= C::A_STAGES;
+                    pa ^= 1;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp < kPEpiWarps) {
+        // ---------------- epilogue: this lane's row is 32 (w % 4) + lane; columns of half w / 4 of
+        // every 128, 32 a step
+        const int q = warp & 3, half = warp >> 2;
+        const uint32_t my = smem_u32(stg + warp * C::STEP_BYTES * (DX ? 2 : 1));
+        const int myrow = 32 * q + lane;
+        const int R4 = lane >> 2, j4 = lane & 3;
+        const uint32_t swz = (lane >> 1) & 3;
+        T* out = static_cast<T*>(A.out);
+        auto tile_code = [&](int tile) -> int {
+            int cls, row0, nrows;
+            tile_rows(tile, cls, row0, nrows);
+            return myrow < nrows ? A.list[row0 + myrow] : -1;
+        };
+        auto fetch_x = [&](int code, int col, int b) {  // as in pair_kernel
+            const T* xs = static_cast<const T*>(A.other);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int R = it * 8 + R4;
+                const int c = __shfl_sync(kFull, code, R);
+                cp_async_16(my + b * C::STEP_BYTES + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4),
+                            xs + static_cast<int64_t>(c < 0 ? 0 : c >> 1) * H + col + j4 * 8, c < 0 ? 0u : 16u);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // the warp's steps of a tile: columns 128 ns + 64 half + 32 i below H
+        auto first_col = half * 64;
+        int tile = blockIdx.x;
+        int next = tile < ntiles ? tile_code(tile) : -1;
+        int xb = 0;
+        if (DX && A.other && tile < ntiles && first_col < H) fetch_x(next, first_col, 0);
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        bool ok = true;
+        for (; tile < ntiles && ok; tile += gridDim.x) {
+            const int code = next, next_tile = tile + gridDim.x;
+            // weight of the lower expert, of the higher
+            const float wl = code >= 0 ? A.weights[code] : 0.0f, wh = code >= 0 ? A.weights[code ^ 1] : 0.0f;
+            if (next_tile < ntiles) next = tile_code(next_tile);
+            int e0 = 0, e1 = 0;
+            if (!DX && A.bias) {
+                const int cls = span_of(ctl->tstart, n, tile);
+                e0 = cls / A.E;
+                e1 = cls % A.E;
+            }
+            uint8_t* dst[4];
+            unsigned there = 0;
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int c = __shfl_sync(kFull, code, it * 8 + R4);
+                there |= c >= 0 ? 1u << it : 0u;
+                dst[it] = reinterpret_cast<uint8_t*>(out) + (static_cast<int64_t>(c < 0 ? 0 : c >> 1) * H + j4 * 8) * 2;
+            }
+            float dl = 0.0f, dh = 0.0f;
+            for (int ns = 0; ns < NS && ok; ++ns) {
+                if (!(ok = mbar_wait(&ctl->tfull[buf], buf_phase, abort, A.flags))) break;
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t tb = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf * 256 + half * 64);
+                const int steps = min(2, (H - ns * 128 - half * 64) / 32);  // 0 or 2: H is a multiple of 64
+                for (int i = 0; i < steps; ++i) {
+                    const int col = ns * 128 + half * 64 + 32 * i;
+                    uint32_t ta[32], th[32];
+                    tmem_ld_32x32b_x32_async(tb + 32 * i, ta);
+                    tmem_ld_32x32b_x32_async(tb + 128 + 32 * i, th);
+                    const uint32_t stage = my + (DX ? xb * C::STEP_BYTES : 0);
+                    if (DX && A.other) {
+                        // the next step's rows of x: of this tile, or the first of the next
+                        const int ncol = i == 0 ? col + 32 : col + 96;
+                        if (ncol < H) fetch_x(code, ncol, xb ^ 1);
+                        else if (next_tile < ntiles) fetch_x(next, first_col, xb ^ 1);
+                        else asm volatile("cp.async.commit_group;" ::: "memory");
+                    }
+                    tmem_ld_wait_tied(ta);
+                    tmem_ld_wait_tied(th);
+                    if (i == 1) {  // the columns are read: the next ones may have the accumulators
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->tempty[buf]);
+                    }
+                    if (DX) {
+                        if (A.other) {
+                            asm volatile("cp.async.wait_group 1;" ::: "memory");
+                            __syncwarp();
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const uint4 raw = ld_shared_u4(stage + lane * 64 + ((g ^ swz) << 4));
+                                const T* xv = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const float xf = to_f(xv[j]);
+                                    dl += __uint_as_float(ta[8 * g + j]) * xf;
+                                    dh += __uint_as_float(th[8 * g + j]) * xf;
+                                }
+                            }
+                        }
+                        xb ^= 1;
+                        if (!out) {
+                            __syncwarp();
+                            continue;
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float s[8];
+                        if (!DX && A.bias) {
+                            const Chunk<T, 8> bl = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.bias) + static_cast<int64_t>(e0) * H + col + 8 * g);
+                            const Chunk<T, 8> bh = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.bias) + static_cast<int64_t>(e1) * H + col + 8 * g);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                s[j] = wl * (__uint_as_float(ta[8 * g + j]) + to_f(bl.v[j])) + wh * (__uint_as_float(th[8 * g + j]) + to_f(bh.v[j]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                s[j] = wl * __uint_as_float(ta[8 * g + j]) + wh * __uint_as_float(th[8 * g + j]);
+                        }
+                        st_shared_u4(stage + lane * 64 + ((g ^ swz) << 4), pack8<T>(s));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) {
+                        const int R = it * 8 + R4;
+                        const uint4 val = ld_shared_u4(stage + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4));
+                        if ((there >> it) & 1u) *reinterpret_cast<uint4*>(dst[it] + 2 * col) = val;
+                    }
+                    __syncwarp();
+                }
+                if (steps == 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->tempty[buf]);
+                }
+                buf ^= 1;
+                if (buf == 0) buf_phase ^= 1;
+            }
+            if (DX && A.other && ok && code >= 0) {
+                A.dw_part[static_cast<int64_t>(half) * A.P + code] = dl;
+                A.dw_part[static_cast<int64_t>(half) * A.P + (code ^ 1)] = dh;
+            }
         }
         if (DX) asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -1206,9 +1673,54 @@ cudaError_t join_launch(const JoinArgs& a, int sms, cudaStream_t s) {
     return go(join_kernel<T, 16, 1, DW>, 1);
 }
 
+// Whether the tokens are grouped by their two experts: few enough pairs of experts that
+// their tiles are mostly full.
+bool takes_duo(const int32_t* expert_idx, int64_t T_, int E, int K, int H) {
+    return K == 2 && expert_idx && aligned(expert_idx, 8) && H <= kDuoMaxH && E <= kDuoMaxE && T_ >= static_cast<int64_t>(512) * E * (E + 1) / 2;
+}
+
+template <typename T, bool DX>
+cudaError_t duo_launch(const void* W, moe_dtype_t dtype, DuoArgs a, const DuoWs& ws, const int32_t* expert_idx, int64_t T_,
+                       int sms, cudaStream_t s) {
+    CUtensorMap map;
+    if (!weight_map(&map, W, dtype, static_cast<uint64_t>(a.E) * a.H, a.H, DX ? 64 : 128)) return cudaErrorInvalidValue;
+    auto kernel = duo_kernel<T, DX>;
+    static std::atomic<uint64_t> ready;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), duo_smem<DX>(), ready);
+    const int n = a.E * a.E;
+    if (e == cudaSuccess) e = cudaMemsetAsync(ws.count, 0, sizeof(int32_t) * 2 * n, s);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>((T_ + kDuoTokens - 1) / kDuoTokens));
+    e = launch_pdl(duo_count_kernel, grid, dim3(256), 0, s, expert_idx, T_, a.E, ws.count);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(duo_group_kernel, grid, dim3(256), 0, s, expert_idx, T_, a.E, ws.count, ws.count + n, ws.count + 2 * n, ws.list);
+    if (e != cudaSuccess) return e;
+    a.start = ws.count + 2 * n;
+    a.list = ws.list;
+    const int64_t tiles = T_ / 128 + n;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kPairThreads), duo_smem<DX>(), s, map, a);
+}
+
+DuoArgs duo_args(const PairArgs& a) {
+    DuoArgs d{};
+    d.src = a.src;
+    d.other = a.other;
+    d.bias = a.bias;
+    d.weights = a.weights;
+    d.E = a.E;
+    d.H = a.H;
+    d.P = a.P;
+    d.out = a.out;
+    d.dw_part = a.dw_part;
+    d.flags = a.flags;
+    return d;
+}
+
 template <typename T>
 cudaError_t fwd_type(const void* W, moe_dtype_t dtype, const PairArgs& a, int64_t T_, const int32_t* expert_idx, int sms,
                      cudaStream_t s) {
+    if (takes_duo(expert_idx, T_, a.E, a.K, a.H))
+        return duo_launch<T, false>(W, dtype, duo_args(a), a.duo, expert_idx, T_, sms, s);
     int parts = 0;
     cudaError_t e = pair_width<T, false>(W, dtype, a, sms, s, &parts);
     if (e != cudaSuccess || a.K == 1) return e;
@@ -1254,13 +1766,15 @@ cudaError_t bwd_type(const void* W, const void* bias, moe_dtype_t dtype, PairArg
                      const int32_t* expert_idx, float* d_weights, int sms, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     if (a.out || d_weights) {
-        int parts = 0;
-        e = pair_width<T, true>(W, dtype, a, sms, s, &parts);
-        if (e == cudaSuccess && (d_weights || a.K > 1)) {
+        const bool duo = takes_duo(expert_idx, T_, a.E, a.K, a.H);
+        int parts = 2;
+        e = duo ? duo_launch<T, true>(W, dtype, duo_args(a), a.duo, expert_idx, T_, sms, s)
+                : pair_width<T, true>(W, dtype, a, sms, s, &parts);
+        if (e == cudaSuccess && (d_weights || (a.K > 1 && !duo))) {
             JoinArgs j{};
             j.rows = a.rows;
             j.scale = a.scale;
-            j.out = a.K > 1 ? a.out : nullptr;
+            j.out = a.K > 1 && !duo ? a.out : nullptr;
             j.dw_part = a.dw_part;
             j.parts = parts;
             j.g = a.src;
@@ -1329,6 +1843,7 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
     a.out = y;
     a.rows = reinterpret_cast<__half*>(ws + L.rows);
     a.scale = reinterpret_cast<float*>(ws + L.scale);
+    a.duo = {reinterpret_cast<int32_t*>(ws + L.duo), reinterpret_cast<int32_t*>(ws + L.list)};
     a.flags = reinterpret_cast<uint32_t*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(dtype == MOE_DTYPE_BF16 ? fwd_type<__nv_bfloat16>(W, dtype, a, T, routing->expert_idx, sms, s)
@@ -1386,6 +1901,7 @@ moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dt
     a.out = d_x;
     a.rows = reinterpret_cast<__half*>(ws + L.rows);
     a.scale = reinterpret_cast<float*>(ws + L.scale);
+    a.duo = {reinterpret_cast<int32_t*>(ws + L.duo), reinterpret_cast<int32_t*>(ws + L.list)};
     a.dw_part = reinterpret_cast<float*>(ws + L.dw_part);
     a.flags = reinterpret_cast<uint32_t*>(ws);
     WgradArgs g{};

@@ -41,6 +41,8 @@ struct ExpertsWs {
     size_t rows = 0;     // fp16 [T * K][H]: the pairs' rows, K > 1
     size_t scale = 0;    // float [T * K][H / 32]: their factors, K > 1
     size_t dw_part = 0;  // float [ceil(H / 64) + 1][T * K]: column parts of the weights' gradient
+    size_t duo = 0;      // int32 [3 * E * E + 1], K = 2: classes of tokens
+    size_t list = 0;     // int32 [T], K = 2: tokens by class
     size_t part = 0;     // float [2 * extra][H][H]
     size_t part_db = 0;  // float [2 * extra][H]
     size_t total = 0;
@@ -59,6 +61,8 @@ inline ExpertsWs experts_ws(int64_t T, int E, int K, int H, size_t begin) {
     L.rows = take(K > 1 ? 2 * P * H : 0);
     L.scale = take(K > 1 ? sizeof(float) * P * (H / 32) : 0);
     L.dw_part = take(sizeof(float) * nb * P);
+    L.duo = take(K == 2 ? sizeof(int32_t) * (3 * static_cast<size_t>(E) * E + 1) : 0);
+    L.list = take(K == 2 ? sizeof(int32_t) * T : 0);
     L.part = take(sizeof(float) * slots * H * H);
     L.part_db = take(sizeof(float) * slots * H);
     L.total = off;

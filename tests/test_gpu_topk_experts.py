@@ -181,7 +181,8 @@ def test_backward(T, E, K, H):
 
 
 @pytest.mark.parametrize("T,E,K,H,skew", [(40000, 8, 2, 256, 1.0), (30000, 3, 2, 128, 0.3), (4000, 32, 4, 1024, 2.0),
-                                          (20001, 60, 6, 64, 1.0), (6000, 2, 1, 512, 4.0)])
+                                          (20001, 60, 6, 64, 1.0), (6000, 2, 1, 512, 4.0),
+                                          (20000, 4, 2, 192, 1.5), (9001, 2, 2, 256, 0.0), (70000, 9, 2, 128, 0.5)])
 def test_many_pairs_and_uneven_experts(T, E, K, H, skew):
     """Several tiles per block, experts cut into pieces and whole ones, experts without a pair."""
     x, W, b, g = _data(T, E, K, H, BF16)
@@ -205,7 +206,8 @@ def _small_integers(T, E, K, H, seed):
     return tri(T, H), W, tri(E, H), tri(T, H), w
 
 
-@pytest.mark.parametrize("T,E,K,H", [(200, 4, 2, 128), (333, 6, 3, 256), (50, 5, 1, 64), (150, 3, 2, 320), (100, 4, 4, 1024)])
+@pytest.mark.parametrize("T,E,K,H", [(200, 4, 2, 128), (333, 6, 3, 256), (50, 5, 1, 64), (150, 3, 2, 320), (100, 4, 4, 1024),
+                                     (7001, 3, 2, 192), (6000, 2, 2, 256), (9000, 4, 2, 64)])
 def test_exact_on_small_integers(T, E, K, H):
     x, W, b, g, w = _small_integers(T, E, K, H, T)
     routing, _ = _routing(T, E, K, T)
@@ -238,9 +240,10 @@ def _routing_of(idx, E):
                        torch.sort(flat, stable=True)[1].to(i))
 
 
-@pytest.mark.parametrize("H", [64, 256])
-def test_everything_on_one_expert_and_the_same_expert_twice(H):
-    T, E, K = 400, 6, 2
+@pytest.mark.parametrize("T,E,H", [(400, 6, 64), (400, 6, 256), (20000, 6, 256), (15000, 7, 192)])
+def test_everything_on_one_expert_and_the_same_expert_twice(T, E, H):
+    """The larger ones group their tokens by pairs of experts."""
+    K = 2
     x, W, b, g = _data(T, E, K, H, BF16)
     w = torch.rand(T, K, device="cuda")
     for idx in (torch.tensor([[2, 5]]).repeat(T, 1), torch.tensor([[3, 3]]).repeat(T, 1)):
@@ -252,6 +255,19 @@ def test_everything_on_one_expert_and_the_same_expert_twice(H):
         none = torch.bincount(idx.reshape(-1), minlength=E) == 0
         assert not got["dW"][none].any() and not got["db"][none].any()
         _check_bwd(got, o, routing, K, H)
+
+
+def test_expert_indices_off_eight_bytes():
+    """Pairs of indices are read together only where they start on 8 bytes."""
+    T, E, K, H = 20000, 4, 2, 128
+    x, W, b, g = _data(T, E, K, H, BF16)
+    routing, w = _routing(T, E, K)
+    off = torch.empty(T * K + 1, dtype=torch.int32, device="cuda")[1:]
+    off.copy_(routing.expert_idx)
+    moved = ops.Routing(off, routing.counts, routing.offsets, routing.perm)
+    o = _reference(x, W, b, g, routing.expert_idx, w)
+    _check_rows("y", _fwd(x, W, b, moved, w), o, K, H)
+    _check_bwd(_bwd(x, W, b, g, moved, w), o, moved, K, H)
 
 
 def test_weights_of_zero_and_negative_weights():
@@ -293,10 +309,10 @@ def test_no_tokens():
     assert not dW.any() and not db.any()
 
 
-def test_repeats_bit_for_bit_with_one_workspace():
+@pytest.mark.parametrize("T,E,K,H", [(9000, 8, 3, 256), (30000, 5, 2, 256)])
+def test_repeats_bit_for_bit_with_one_workspace(T, E, K, H):
     """Whatever the order in which a token's rows come in: the same bits, call after call, and with
     another size through the same workspace in between; on another stream; captured and replayed."""
-    T, E, K, H = 9000, 8, 3, 256
     x, W, b, g = _data(T, E, K, H, BF16)
     routing, w = _routing(T, E, K)
     ws = ops.new_topk_workspace(T, E, K, H, "cuda")
