@@ -45,14 +45,36 @@ namespace {
 constexpr int kMaxE = 256, kMaxK = 16, kMaxH = 4096;
 constexpr unsigned kFull = 0xffffffffu;
 
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x;
+}
+// A wait of a whole warp whose outcome is the same in every lane for the compiler too.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* flags) {
+    return __all_sync(kFull, mbar_wait(bar, parity, abort, flags));
+}
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (both operands fp16 or both bf16), fp32 sums.
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// The whole warp comes here with the same operands, which then sit in uniform registers as
+// the instruction wants them, and the elected lane issues. The descriptors come as words:
+// the upper ones are constants, the lower ones a constant plus the operand's address / 16.
+__device__ __forceinline__ void mma_f16(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                        uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "mov.b64 da, {%1, %2};\n\t"
+        "mov.b64 db, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit_f16(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(leader)
         : "memory");
 }
 
@@ -75,9 +97,13 @@ __device__ __forceinline__ uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) 
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// MN-major 16-bit operand, 128-byte swizzle: rows along K of 64 elements (128 bytes) of M or N; 8-row groups along K
-// are 1024 bytes apart (SBO), groups of 64 elements along M or N lbo_bytes apart.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t lbo_bytes) { return sw128_desc(addr, lbo_bytes, 1024); }
+// Descriptor words of 16-bit operands in the 128-byte swizzle, 8-row groups 1024 bytes
+// apart. K-major: rows of 64 elements along K; 16 of them are 32 bytes on. MN-major: rows
+// along K of 64 elements of M or N, groups of 64 along M or N lbo bytes apart; 16 rows are
+// 2048 bytes on. (The layout of sw128_desc.)
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kKStep = 32 >> 4, kMnStep = 2048 >> 4;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo_bytes) { return (addr >> 4) | ((lbo_bytes >> 4) << 16); }
 
 template <typename T>
 __device__ __forceinline__ uint4 pack8(const float (&s)[8]) {
@@ -333,32 +359,31 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
         }
         __syncwarp();
     } else if (warp == kPMmaWarp) {
-        // ---------------- MMA issuer (one thread)
-        if (lane == 0) {
+        // ---------------- MMA issuer (the warp stays together, one lane issues)
+        {
+            const uint32_t leader = elect_one();
+            const uint32_t a0 = desc_lo(smem_u32(aring), 16), b0 = desc_lo(smem_u32(bring), DX ? 64 * 128 : 16);
             int sa = 0, sb = 0;
             uint32_t pa = 0, pb = 0;
             int acc = 0;
             uint32_t acc_phase = 0;
             bool ok = true;
             for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-                if (!(ok = mbar_wait(&ctl->tempty[acc], acc_phase ^ 1, abort, A.flags))) break;
+                if (!(ok = warp_wait(&ctl->tempty[acc], acc_phase ^ 1, abort, A.flags))) break;
                 tc_fence_after();
                 const uint32_t idesc = idesc_f16<T>(128, min(BN, H - (tile % NT) * BN), 0, DX ? 1 : 0);
                 const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
                 for (int kc = 0; kc < KCH; ++kc) {
-                    if (!(ok = mbar_wait(&ctl->afull[sa], pa, abort, A.flags))) break;
-                    if (!(ok = mbar_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
+                    if (!(ok = warp_wait(&ctl->afull[sa], pa, abort, A.flags))) break;
+                    if (!(ok = warp_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
                     fence_proxy_async_smem();
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(aring + sa * C::A_BYTES);
-                    const uint32_t b_addr = smem_u32(bring + sb * C::B_BYTES);
+                    const uint32_t a = a0 + sa * (C::A_BYTES >> 4), b = b0 + sb * (C::B_BYTES >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const uint64_t bdesc = DX ? mn_desc(b_addr + ks * 2048, 64 * 128) : sw128_desc(b_addr + ks * 32, 16, 1024);
-                        mma_f16(d, sw128_desc(a_addr + ks * 32, 16, 1024), bdesc, idesc, (kc | ks) != 0 ? 1u : 0u);
-                    }
-                    mma_commit(&ctl->aempty[sa]);
-                    mma_commit(&ctl->bempty[sb]);
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f16(leader, d, a + ks * kKStep, kDescHi, b + ks * (DX ? kMnStep : kKStep), kDescHi, idesc, ks != 0 ? 1u : kc != 0);
+                    commit_f16(leader, &ctl->aempty[sa]);
+                    commit_f16(leader, &ctl->bempty[sb]);
                     if (++sa == C::A_STAGES) {
                         sa = 0;
                         pa ^= 1;
@@ -369,7 +394,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                     }
                 }
                 if (!ok) break;
-                mma_commit(&ctl->tfull[acc]);
+                commit_f16(leader, &ctl->tfull[acc]);
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1;
             }
@@ -803,9 +828,11 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
         }
         __syncwarp();
     } else if (warp == kPMmaWarp) {
-        // ---------------- MMA issuer (one thread): accumulators of expert s, columns step, at
+        // ---------------- MMA issuer: accumulators of expert s, columns step, at
         // 256 buf + 128 s
-        if (lane == 0) {
+        {
+            const uint32_t leader = elect_one();
+            const uint32_t a0 = desc_lo(smem_u32(aring), 16), b0 = desc_lo(smem_u32(bring), DX ? 64 * 128 : 16);
             int sa = 0, sb = 0;
             uint32_t pa = 0, pb = 0;
             int buf = 0;
@@ -813,7 +840,7 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
             bool ok = true;
             for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
                 for (int ns = 0; ns < NS && ok; ++ns) {
-                    if (!(ok = mbar_wait(&ctl->tempty[buf], buf_phase ^ 1, abort, A.flags))) break;
+                    if (!(ok = warp_wait(&ctl->tempty[buf], buf_phase ^ 1, abort, A.flags))) break;
                     tc_fence_after();
                     const uint32_t idesc = idesc_f16<T>(128, min(128, H - ns * 128), 0, DX ? 1 : 0);
                     for (int s = 0; s < 2 && ok; ++s) {
@@ -822,20 +849,17 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
                             const int a = (sa + kc) % C::A_STAGES;
                             if (ns == 0 && s == 0) {
                                 const uint32_t ph = pa ^ (sa + kc >= C::A_STAGES ? 1u : 0u);
-                                if (!(ok = mbar_wait(&ctl->afull[a], ph, abort, A.flags))) break;
+                                if (!(ok = warp_wait(&ctl->afull[a], ph, abort, A.flags))) break;
                             }
-                            if (!(ok = mbar_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
+                            if (!(ok = warp_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
                             fence_proxy_async_smem();
                             tc_fence_after();
-                            const uint32_t a_addr = smem_u32(aring + a * C::A_BYTES);
-                            const uint32_t b_addr = smem_u32(bring + sb * C::B_BYTES);
+                            const uint32_t al = a0 + a * (C::A_BYTES >> 4), bl = b0 + sb * (C::B_BYTES >> 4);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) {
-                                const uint64_t bdesc = DX ? mn_desc(b_addr + ks * 2048, 64 * 128) : sw128_desc(b_addr + ks * 32, 16, 1024);
-                                mma_f16(d, sw128_desc(a_addr + ks * 32, 16, 1024), bdesc, idesc, (kc | ks) != 0 ? 1u : 0u);
-                            }
-                            mma_commit(&ctl->bempty[sb]);
-                            if (ns == NS - 1 && s == 1) mma_commit(&ctl->aempty[a]);
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_f16(leader, d, al + ks * kKStep, kDescHi, bl + ks * (DX ? kMnStep : kKStep), kDescHi, idesc, ks != 0 ? 1u : kc != 0);
+                            commit_f16(leader, &ctl->bempty[sb]);
+                            if (ns == NS - 1 && s == 1) commit_f16(leader, &ctl->aempty[a]);
                             if (++sb == C::B_STAGES) {
                                 sb = 0;
                                 pb ^= 1;
@@ -843,7 +867,7 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
                         }
                     }
                     if (!ok) break;
-                    mma_commit(&ctl->tfull[buf]);
+                    commit_f16(leader, &ctl->tfull[buf]);
                     buf ^= 1;
                     if (buf == 0) buf_phase ^= 1;
                 }
@@ -1336,7 +1360,9 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         }
     } else if (warp == kWMmaWarp) {
         // ---------------- MMA issuer: two halves of 128 rows of dW, the tile's columns
-        if (lane == 0) {
+        {
+            const uint32_t leader = elect_one();
+            const uint32_t g0 = desc_lo(smem_u32(smem), C::GROUP);
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
@@ -1344,26 +1370,28 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                 const Unit r = unit_of(u);
                 const int halves = (min(kWTile, H - r.o0) + 127) / 128;
                 const uint32_t idesc = idesc_f16<T>(128, min(kWTile, H - r.i0), 1, 1);
-                if (!(ok = mbar_wait(&ctl->tempty, acc_phase ^ 1, abort, A.flags))) break;
+                if (!(ok = warp_wait(&ctl->tempty, acc_phase ^ 1, abort, A.flags))) break;
                 tc_fence_after();
                 for (int p0 = r.lo; p0 < r.hi; p0 += C::KT) {
-                    if (!(ok = mbar_wait(&ctl->full[stage], phase, abort, A.flags))) break;
+                    if (!(ok = warp_wait(&ctl->full[stage], phase, abort, A.flags))) break;
                     fence_proxy_async_smem();
                     tc_fence_after();
-                    const uint32_t g_addr = smem_u32(smem + stage * C::STAGE), x_addr = g_addr + C::OP;
+                    const uint32_t gl = g0 + stage * (C::STAGE >> 4), xl = gl + (C::OP >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < C::KT / 16; ++ks)
-                        for (int mh = 0; mh < halves; ++mh)
-                            mma_f16(tmem + static_cast<uint32_t>(mh * 256), mn_desc(g_addr + mh * 2 * C::GROUP + ks * 2048, C::GROUP),
-                                    mn_desc(x_addr + ks * 2048, C::GROUP), idesc, (p0 != r.lo || ks != 0) ? 1u : 0u);
-                    mma_commit(&ctl->empty[stage]);
+                    for (int ks = 0; ks < C::KT / 16; ++ks) {
+                        const uint32_t on = ks != 0 ? 1u : p0 != r.lo;
+                        mma_f16(leader, tmem, gl + ks * kMnStep, kDescHi, xl + ks * kMnStep, kDescHi, idesc, on);
+                        if (halves == 2)
+                            mma_f16(leader, tmem + 256, gl + (2 * C::GROUP >> 4) + ks * kMnStep, kDescHi, xl + ks * kMnStep, kDescHi, idesc, on);
+                    }
+                    commit_f16(leader, &ctl->empty[stage]);
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                mma_commit(&ctl->tfull);
+                commit_f16(leader, &ctl->tfull);
                 acc_phase ^= 1;
             }
         }
