@@ -78,6 +78,23 @@ __device__ __forceinline__ void commit_f16(uint32_t leader, uint64_t* bar) {
         : "memory");
 }
 
+// The elected lane expects `bytes` on the barrier; loads one box.
+__device__ __forceinline__ void expect_f16(uint32_t leader, uint64_t* bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(bytes), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1,
+                                         uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "r"(leader)
+        : "memory");
+}
+
 template <typename T>
 struct MmaFormat;
 template <>
@@ -330,7 +347,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
     } else if (warp == kPLoadWarp) {
         // ---------------- weight loader. Boxes may reach past the expert's last row or column block
         // (H not a multiple of BN): those columns of the accumulator are not used.
-        if (lane == 0) {
+        {
+            const uint32_t leader = elect_one(), ring = smem_u32(bring);
             int sb = 0;
             uint32_t pb = 0;
             bool ok = true;
@@ -340,15 +358,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                 const int n0 = (tile % NT) * BN;
                 const int ng = DX ? min(BN, H - n0) / 64 : 0;
                 for (int kc = 0; kc < KCH; ++kc) {
-                    if (!(ok = mbar_wait(&ctl->bempty[sb], pb ^ 1, abort, A.flags))) break;
+                    if (!(ok = warp_wait(&ctl->bempty[sb], pb ^ 1, abort, A.flags))) break;
                     if (DX) {
-                        mbar_arrive_expect_tx(&ctl->bfull[sb], ng * 64 * 128);
+                        expect_f16(leader, &ctl->bfull[sb], ng * 64 * 128);
                         for (int g = 0; g < ng; ++g)
-                            tma_load_2d(bring + sb * C::B_BYTES + g * 64 * 128, &tm_w, n0 + g * 64, e * H + kc * 64,
+                            load_box(leader, ring + sb * C::B_BYTES + g * 64 * 128, &tm_w, n0 + g * 64, e * H + kc * 64,
                                         &ctl->bfull[sb]);
                     } else {
-                        mbar_arrive_expect_tx(&ctl->bfull[sb], C::B_BYTES);
-                        tma_load_2d(bring + sb * C::B_BYTES, &tm_w, kc * 64, e * H + n0, &ctl->bfull[sb]);
+                        expect_f16(leader, &ctl->bfull[sb], C::B_BYTES);
+                        load_box(leader, ring + sb * C::B_BYTES, &tm_w, kc * 64, e * H + n0, &ctl->bfull[sb]);
                     }
                     if (++sb == C::B_STAGES) {
                         sb = 0;
@@ -660,13 +678,15 @@ duo_group_kernel(const int32_t* __restrict__ expert_idx, int64_t T_, int E, cons
 }
 
 // Warps as in pair_kernel. A tile's rows (all of H, at most 4 chunks of 64 columns) stay in
-// shared memory while both experts' weights pass by, 128 output columns at a time; the two
-// accumulators of those columns are one half of tensor memory.
+// shared memory while both experts' weights pass by, 128 output columns at a time: 128
+// rows of either expert's W are one operand of 256, so one MMA does both, and its 256
+// accumulator columns are one half of tensor memory. (Where fewer than 128 columns are
+// left, the rest of either half is computed from what lies there and not used.)
 template <bool DX>
 struct DuoCfg {
-    static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
-    static constexpr int A_STAGES = 8;  // two tiles of 256 columns
-    static constexpr int B_STAGES = DX ? 3 : 4;
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = 256 * 128;
+    static constexpr int A_STAGES = DX ? 5 : 6;  // a tile of 256 columns and a part of the next
+    static constexpr int B_STAGES = 3;
     static constexpr int RING_BYTES = A_STAGES * A_BYTES + B_STAGES * B_BYTES;
     static constexpr int STEP_BYTES = 32 * 64;
     static constexpr int STG_BYTES = kPEpiWarps * STEP_BYTES * (DX ? 2 : 1);
@@ -796,27 +816,30 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
         }
     } else if (warp == kPLoadWarp) {
         // ---------------- weight loader: columns, experts, chunks in the MMAs' order
-        if (lane == 0) {
+        {
+            const uint32_t leader = elect_one(), ring = smem_u32(bring);
             int sb = 0;
             uint32_t pb = 0;
             bool ok = true;
             for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
                 int cls, row0, nrows;
                 tile_rows(tile, cls, row0, nrows);
-                const int e2[2] = {cls / A.E, cls % A.E};
-                for (int step = 0; step < NS * 2 && ok; ++step) {
-                    const int n0 = (step >> 1) * 128, e = e2[step & 1];
+                const int lo = cls / A.E * H, hi = cls % A.E * H;  // the experts' first rows
+                for (int n0 = 0; n0 < H && ok; n0 += 128) {
                     const int ng = min(128, H - n0) / 64;
                     for (int kc = 0; kc < KCH; ++kc) {
-                        if (!(ok = mbar_wait(&ctl->bempty[sb], pb ^ 1, abort, A.flags))) break;
+                        if (!(ok = warp_wait(&ctl->bempty[sb], pb ^ 1, abort, A.flags))) break;
+                        const uint32_t b = ring + sb * C::B_BYTES;
                         if (DX) {
-                            mbar_arrive_expect_tx(&ctl->bfull[sb], ng * 64 * 128);
-                            for (int g = 0; g < ng; ++g)
-                                tma_load_2d(bring + sb * C::B_BYTES + g * 64 * 128, &tm_w, n0 + g * 64, e * H + kc * 64,
-                                            &ctl->bfull[sb]);
+                            expect_f16(leader, &ctl->bfull[sb], 2 * ng * 64 * 128);
+                            for (int g = 0; g < ng; ++g) {
+                                load_box(leader, b + g * 64 * 128, &tm_w, n0 + g * 64, lo + kc * 64, &ctl->bfull[sb]);
+                                load_box(leader, b + (g + 2) * 64 * 128, &tm_w, n0 + g * 64, hi + kc * 64, &ctl->bfull[sb]);
+                            }
                         } else {
-                            mbar_arrive_expect_tx(&ctl->bfull[sb], C::B_BYTES);
-                            tma_load_2d(bring + sb * C::B_BYTES, &tm_w, kc * 64, e * H + n0, &ctl->bfull[sb]);
+                            expect_f16(leader, &ctl->bfull[sb], C::B_BYTES);
+                            load_box(leader, b, &tm_w, kc * 64, lo + n0, &ctl->bfull[sb]);
+                            load_box(leader, b + 128 * 128, &tm_w, kc * 64, hi + n0, &ctl->bfull[sb]);
                         }
                         if (++sb == C::B_STAGES) {
                             sb = 0;
@@ -828,8 +851,8 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
         }
         __syncwarp();
     } else if (warp == kPMmaWarp) {
-        // ---------------- MMA issuer: accumulators of expert s, columns step, at
-        // 256 buf + 128 s
+        // ---------------- MMA issuer: sums of 128 columns of the lower expert at 256 buf, of the higher
+        // 128 columns on
         {
             const uint32_t leader = elect_one();
             const uint32_t a0 = desc_lo(smem_u32(aring), 16), b0 = desc_lo(smem_u32(bring), DX ? 64 * 128 : 16);
@@ -837,33 +860,31 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
             uint32_t pa = 0, pb = 0;
             int buf = 0;
             uint32_t buf_phase = 0;
+            const uint32_t idesc = idesc_f16<T>(128, 256, 0, DX ? 1 : 0);
             bool ok = true;
             for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
                 for (int ns = 0; ns < NS && ok; ++ns) {
                     if (!(ok = warp_wait(&ctl->tempty[buf], buf_phase ^ 1, abort, A.flags))) break;
                     tc_fence_after();
-                    const uint32_t idesc = idesc_f16<T>(128, min(128, H - ns * 128), 0, DX ? 1 : 0);
-                    for (int s = 0; s < 2 && ok; ++s) {
-                        const uint32_t d = tmem + static_cast<uint32_t>(buf * 256 + s * 128);
-                        for (int kc = 0; kc < KCH; ++kc) {
-                            const int a = (sa + kc) % C::A_STAGES;
-                            if (ns == 0 && s == 0) {
-                                const uint32_t ph = pa ^ (sa + kc >= C::A_STAGES ? 1u : 0u);
-                                if (!(ok = warp_wait(&ctl->afull[a], ph, abort, A.flags))) break;
-                            }
-                            if (!(ok = warp_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
-                            fence_proxy_async_smem();
-                            tc_fence_after();
-                            const uint32_t al = a0 + a * (C::A_BYTES >> 4), bl = b0 + sb * (C::B_BYTES >> 4);
+                    const uint32_t d = tmem + static_cast<uint32_t>(buf * 256);
+                    for (int kc = 0; kc < KCH; ++kc) {
+                        const int a = sa + kc >= C::A_STAGES ? sa + kc - C::A_STAGES : sa + kc;
+                        if (ns == 0) {
+                            const uint32_t ph = pa ^ (sa + kc >= C::A_STAGES ? 1u : 0u);
+                            if (!(ok = warp_wait(&ctl->afull[a], ph, abort, A.flags))) break;
+                        }
+                        if (!(ok = warp_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
+                        fence_proxy_async_smem();
+                        tc_fence_after();
+                        const uint32_t al = a0 + a * (C::A_BYTES >> 4), bl = b0 + sb * (C::B_BYTES >> 4);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_f16(leader, d, al + ks * kKStep, kDescHi, bl + ks * (DX ? kMnStep : kKStep), kDescHi, idesc, ks != 0 ? 1u : kc != 0);
-                            commit_f16(leader, &ctl->bempty[sb]);
-                            if (ns == NS - 1 && s == 1) commit_f16(leader, &ctl->aempty[a]);
-                            if (++sb == C::B_STAGES) {
-                                sb = 0;
-                                pb ^= 1;
-                            }
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_f16(leader, d, al + ks * kKStep, kDescHi, bl + ks * (DX ? kMnStep : kKStep), kDescHi, idesc, ks != 0 ? 1u : kc != 0);
+                        commit_f16(leader, &ctl->bempty[sb]);
+                        if (ns == NS - 1) commit_f16(leader, &ctl->aempty[a]);
+                        if (++sb == C::B_STAGES) {
+                            sb = 0;
+                            pb ^= 1;
                         }
                     }
                     if (!ok) break;
