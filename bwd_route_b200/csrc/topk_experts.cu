@@ -55,6 +55,13 @@ __device__ __forceinline__ uint32_t elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* flags) {
     return __all_sync(kFull, mbar_wait(bar, parity, abort, flags));
 }
+// Two of them, asked for together: where both are there already, one latency.
+__device__ __forceinline__ bool warp_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* abort,
+                                               uint32_t* flags) {
+    const bool ra = mbar_try_wait(smem_u32(a), pa), rb = mbar_try_wait(smem_u32(b), pb);
+    if (__all_sync(kFull, ra && rb)) return true;
+    return warp_wait(a, pa, abort, flags) && warp_wait(b, pb, abort, flags);
+}
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (both operands fp16 or both bf16), fp32 sums.
 // The whole warp comes here with the same operands, which then sit in uniform registers as
 // the instruction wants them, and the elected lane issues. The descriptors come as words:
@@ -392,8 +399,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                 const uint32_t idesc = idesc_f16<T>(128, min(BN, H - (tile % NT) * BN), 0, DX ? 1 : 0);
                 const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
                 for (int kc = 0; kc < KCH; ++kc) {
-                    if (!(ok = warp_wait(&ctl->afull[sa], pa, abort, A.flags))) break;
-                    if (!(ok = warp_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
+                    if (!(ok = warp_wait_both(&ctl->afull[sa], pa, &ctl->bfull[sb], pb, abort, A.flags))) break;
                     fence_proxy_async_smem();
                     tc_fence_after();
                     const uint32_t a = a0 + sa * (C::A_BYTES >> 4), b = b0 + sb * (C::B_BYTES >> 4);
@@ -701,8 +707,13 @@ struct __align__(8) DuoCtl {
     int start[kDuoMaxE * kDuoMaxE + 1];
     int tstart[kDuoMaxE * kDuoMaxE + 1];
 };
+// y: behind it, for every epilogue warp, the biases of a tile's two experts in its columns, [2][128] fp32.
+constexpr int kDuoBias = 2 * 128 * 4;
 template <bool DX>
-constexpr int duo_smem() { return 1024 + DuoCfg<DX>::RING_BYTES + DuoCfg<DX>::STG_BYTES + static_cast<int>(sizeof(DuoCtl)); }
+constexpr int duo_smem() {
+    return 1024 + DuoCfg<DX>::RING_BYTES + DuoCfg<DX>::STG_BYTES + static_cast<int>(sizeof(DuoCtl)) + 16 +
+           (DX ? 0 : kPEpiWarps * kDuoBias);
+}
 static_assert(duo_smem<false>() <= 227 * 1024 && duo_smem<true>() <= 227 * 1024, "shared memory");
 
 struct DuoArgs {
@@ -869,11 +880,10 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
                     const uint32_t d = tmem + static_cast<uint32_t>(buf * 256);
                     for (int kc = 0; kc < KCH; ++kc) {
                         const int a = sa + kc >= C::A_STAGES ? sa + kc - C::A_STAGES : sa + kc;
-                        if (ns == 0) {
-                            const uint32_t ph = pa ^ (sa + kc >= C::A_STAGES ? 1u : 0u);
-                            if (!(ok = warp_wait(&ctl->afull[a], ph, abort, A.flags))) break;
-                        }
-                        if (!(ok = warp_wait(&ctl->bfull[sb], pb, abort, A.flags))) break;
+                        const uint32_t ph = pa ^ (sa + kc >= C::A_STAGES ? 1u : 0u);
+                        ok = ns == 0 ? warp_wait_both(&ctl->afull[a], ph, &ctl->bfull[sb], pb, abort, A.flags)
+                                     : warp_wait(&ctl->bfull[sb], pb, abort, A.flags);
+                        if (!ok) break;
                         fence_proxy_async_smem();
                         tc_fence_after();
                         const uint32_t al = a0 + a * (C::A_BYTES >> 4), bl = b0 + sb * (C::B_BYTES >> 4);
@@ -926,7 +936,8 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         // the warp's steps of a tile: columns 128 ns + 64 half + 32 i below H
-        auto first_col = half * 64;
+        const int first_col = half * 64;
+        const uint32_t sbias = ((smem_u32(ctl) + static_cast<uint32_t>(sizeof(DuoCtl)) + 15) & ~15u) + warp * kDuoBias;
         int tile = blockIdx.x;
         int next = tile < ntiles ? tile_code(tile) : -1;
         int xb = 0;
@@ -939,11 +950,16 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
             // weight of the lower expert, of the higher
             const float wl = code >= 0 ? A.weights[code] : 0.0f, wh = code >= 0 ? A.weights[code ^ 1] : 0.0f;
             if (next_tile < ntiles) next = tile_code(next_tile);
-            int e0 = 0, e1 = 0;
             if (!DX && A.bias) {
+                // eight columns a lane: expert lane / 16, columns 128 ns + 64 half + 8 (lane % 8)
                 const int cls = span_of(ctl->tstart, n, tile);
-                e0 = cls / A.E;
-                e1 = cls % A.E;
+                const int e = lane < 16 ? cls / A.E : cls % A.E, c = 128 * ((lane >> 3) & 1) + 64 * half + 8 * (lane & 7);
+                Chunk<T, 8> b{};
+                if (c < H) b = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.bias) + static_cast<int64_t>(e) * H + c);
+                const uint32_t to = sbias + (lane >> 3) * 256 + 32 * (lane & 7);
+                st_shared_v4(to, to_f(b.v[0]), to_f(b.v[1]), to_f(b.v[2]), to_f(b.v[3]));
+                st_shared_v4(to + 16, to_f(b.v[4]), to_f(b.v[5]), to_f(b.v[6]), to_f(b.v[7]));
+                __syncwarp();
             }
             uint8_t* dst[4];
             unsigned there = 0;
@@ -1006,11 +1022,17 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
                     for (int g = 0; g < 4; ++g) {
                         float s[8];
                         if (!DX && A.bias) {
-                            const Chunk<T, 8> bl = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.bias) + static_cast<int64_t>(e0) * H + col + 8 * g);
-                            const Chunk<T, 8> bh = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.bias) + static_cast<int64_t>(e1) * H + col + 8 * g);
+                            // the same words for every lane; the higher expert's 512 bytes on
+                            const uint32_t from = sbias + ns * 256 + (32 * i + 8 * g) * 4;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                s[j] = wl * (__uint_as_float(ta[8 * g + j]) + to_f(bl.v[j])) + wh * (__uint_as_float(th[8 * g + j]) + to_f(bh.v[j]));
+                            for (int h = 0; h < 2; ++h) {
+                                const float4 bl = ld_shared_v4(from + 16 * h), bh = ld_shared_v4(from + 512 + 16 * h);
+                                const int j = 8 * g + 4 * h;
+                                s[4 * h] = wl * (__uint_as_float(ta[j]) + bl.x) + wh * (__uint_as_float(th[j]) + bh.x);
+                                s[4 * h + 1] = wl * (__uint_as_float(ta[j + 1]) + bl.y) + wh * (__uint_as_float(th[j + 1]) + bh.y);
+                                s[4 * h + 2] = wl * (__uint_as_float(ta[j + 2]) + bl.z) + wh * (__uint_as_float(th[j + 2]) + bh.z);
+                                s[4 * h + 3] = wl * (__uint_as_float(ta[j + 3]) + bl.w) + wh * (__uint_as_float(th[j + 3]) + bh.w);
+                            }
                         } else {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
@@ -1153,6 +1175,7 @@ constexpr int kMaxPieces = kMaxE + kWUnits;
 
 struct WCfg {
     static constexpr int KT = 32;              // pairs per stage
+    static constexpr int RW = KT / 4;          // rows of a stage a warp gathers, or scales
     static constexpr int GROUP = KT * 128;     // 64 columns of a stage's rows
     static constexpr int OP = 4 * GROUP;       // 256 columns
     static constexpr int STAGE = 2 * OP;       // g then x: 32 KiB
@@ -1337,11 +1360,11 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         int stage = 0, slot = 0;
         uint32_t phase = 0, lphase = 0;
         bool ok = true;
-        // a warp has rows 8 w4 .. 8 w4 + 7 of a stage: row i of them swizzles by i
+        // a warp has rows RW w4 .. of a stage: row i of them swizzles by i % 8
         uint32_t to[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            to[i] = smem_u32(smem) + (lane >> 3) * C::GROUP + (8 * w4 + i) * 128 + (((lane & 7) ^ i) << 4);
+            to[i] = smem_u32(smem) + (lane >> 3) * C::GROUP + (C::RW * w4 + i) * 128 + (((lane & 7) ^ i) << 4);
         for (int turn = 0, u; ok && (u = unit_number(turn)) >= 0; ++turn) {
             const Unit r = unit_of(u);
             const bool on_g = lane * 8 < min(kWTile, H - r.o0), on_x = lane * 8 < min(kWTile, H - r.i0);
@@ -1351,19 +1374,19 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                 if (!(ok = mbar_wait(&ctl->lfull[slot], lphase, abort, A.flags))) break;
                 const int steps = min(C::STEPS, (r.hi - at + C::KT - 1) / C::KT);
                 for (int st = 0; st < steps; ++st) {
-                    longlong2 rows[4];
+                    longlong2 rows[C::RW / 2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        rows[i] = *reinterpret_cast<const longlong2*>(&ctl->row[slot][st * C::KT + 8 * w4 + 2 * i]);
-                    const int left = r.hi - at - st * C::KT - 8 * w4;  // rows of the warp that are pairs
+                    for (int i = 0; i < C::RW / 2; ++i)
+                        rows[i] = *reinterpret_cast<const longlong2*>(&ctl->row[slot][st * C::KT + C::RW * w4 + 2 * i]);
+                    const int left = r.hi - at - st * C::KT - C::RW * w4;  // rows of the warp that are pairs
                     if (!(ok = mbar_wait(&ctl->empty[stage], phase ^ 1, abort, A.flags))) break;
                     const uint32_t base = stage * C::STAGE;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < C::RW; ++i) {
                         const int64_t row = (i & 1) ? rows[i / 2].y : rows[i / 2].x;
-                        const uint32_t bytes = i < left ? 16u : 0u;
-                        if (on_g) cp_async_16(to[i] + base, gl + row, bytes);
-                        if (on_x) cp_async_16(to[i] + base + C::OP, xl + row, bytes);
+                        const uint32_t bytes = i < left ? 16u : 0u, at_i = to[i & 7] + (i >> 3) * 1024 + base;
+                        if (on_g) cp_async_16(at_i, gl + row, bytes);
+                        if (on_x) cp_async_16(at_i + C::OP, xl + row, bytes);
                     }
                     cp_async_arrive_noinc(&ctl->raw[stage]);
                     if (++stage == C::STAGES) {
@@ -1426,13 +1449,13 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
         uint32_t phase = 0, lphase = 0, acc_phase = 0;
         bool ok = true;
         T* dW = static_cast<T*>(A.dW);
-        // warps 0-3 scale the even stages, 4-7 the odd ones (there is an even number), so that one stage's
-        // latency hides behind the other's; rows 8 q .. 8 q + 7, row i of them swizzled by i
-        static_assert(C::STAGES % 2 == 0, "a stage has the same warps every time");
+        // warps 0-3 and 4-7 scale stages in turn, so that one stage's latency hides behind the other's;
+        // rows RW q .., row i of them swizzled by i % 8
+        int turns = 0;
         uint32_t to[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            to[i] = smem_u32(smem) + (lane >> 3) * C::GROUP + (8 * q + i) * 128 + (((lane & 7) ^ i) << 4);
+            to[i] = smem_u32(smem) + (lane >> 3) * C::GROUP + (C::RW * q + i) * 128 + (((lane & 7) ^ i) << 4);
         for (int turn = 0, u; (u = unit_number(turn)) >= 0; ++turn) {
             const Unit r = unit_of(u);
             const int rows = min(kWTile, H - r.o0), cols = min(kWTile, H - r.i0);
@@ -1443,32 +1466,35 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                 if (!(ok = mbar_wait(&ctl->lfull[slot], lphase, abort, A.flags))) break;
                 const int steps = min(C::STEPS, (r.hi - at + C::KT - 1) / C::KT);
                 for (int st = 0; st < steps; ++st) {
-                    if ((stage & 1) == ch) {
-                        float wr[8];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float4 w4 = *reinterpret_cast<const float4*>(&ctl->weight[slot][st * C::KT + 8 * q + 4 * i]);
-                            wr[4 * i] = w4.x;
-                            wr[4 * i + 1] = w4.y;
-                            wr[4 * i + 2] = w4.z;
-                            wr[4 * i + 3] = w4.w;
-                        }
+                    if ((turns++ & 1) == ch) {
                         if (!(ok = mbar_wait(&ctl->raw[stage], phase, abort, A.flags))) break;
-                        const uint32_t base = stage * C::STAGE;
-                        if (on) {
-                            uint4 raw[8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) raw[i] = ld_shared_u4(to[i] + base);
+                        for (int h = 0; h < C::RW / 8; ++h) {
+                            float wr[8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const T* v = reinterpret_cast<const T*>(&raw[i]);
-                                float s[8];
+                            for (int i = 0; i < 2; ++i) {
+                                const float4 w4 = *reinterpret_cast<const float4*>(&ctl->weight[slot][st * C::KT + C::RW * q + 8 * h + 4 * i]);
+                                wr[4 * i] = w4.x;
+                                wr[4 * i + 1] = w4.y;
+                                wr[4 * i + 2] = w4.z;
+                                wr[4 * i + 3] = w4.w;
+                            }
+                            const uint32_t base = stage * C::STAGE + h * 1024;
+                            if (on) {
+                                uint4 raw[8];
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) s[j] = wr[i] * to_f(v[j]);
-                                if (add)
+                                for (int i = 0; i < 8; ++i) raw[i] = ld_shared_u4(to[i] + base);
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j) db[j] += s[j];
-                                st_shared_u4(to[i] + base, pack8<T>(s));
+                                for (int i = 0; i < 8; ++i) {
+                                    const T* v = reinterpret_cast<const T*>(&raw[i]);
+                                    float s[8];
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) s[j] = wr[i] * to_f(v[j]);
+                                    if (add)
+#pragma unroll
+                                        for (int j = 0; j < 8; ++j) db[j] += s[j];
+                                    st_shared_u4(to[i] + base, pack8<T>(s));
+                                }
                             }
                         }
                         fence_proxy_async_smem();
@@ -1722,10 +1748,13 @@ cudaError_t join_launch(const JoinArgs& a, int sms, cudaStream_t s) {
     return go(join_kernel<T, 16, 1, DW>, 1);
 }
 
-// Whether the tokens are grouped by their two experts: few enough pairs of experts that
-// their tiles are mostly full.
+// Whether the tokens are grouped by their two experts. Grouping takes about 13 us, and the
+// tiles of the E (E + 1) / 2 classes have to be mostly full. Forward, rows joined / grouped:
+// E 8, H 256: 36,864 tokens 30.9 / 34.3 us, 73,728: 55.6 / 40.5; E 16, H 128: 69,632 tokens
+// 31.1 / 34.9, 139,264: 56.1 / 45.5; forward and backward together cross at the same sizes.
 bool takes_duo(const int32_t* expert_idx, int64_t T_, int E, int K, int H) {
-    return K == 2 && expert_idx && aligned(expert_idx, 8) && H <= kDuoMaxH && E <= kDuoMaxE && T_ >= static_cast<int64_t>(512) * E * (E + 1) / 2;
+    return K == 2 && expert_idx && aligned(expert_idx, 8) && H <= kDuoMaxH && E <= kDuoMaxE && T_ >= 49152 &&
+           T_ >= 640 * static_cast<int64_t>(E * (E + 1) / 2);
 }
 
 template <typename T, bool DX>

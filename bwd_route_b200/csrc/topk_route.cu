@@ -711,11 +711,21 @@ __device__ __forceinline__ void scatter_pairs(const int* idx, int n, int32_t p0,
     for (int e = lane; e < E; e += 32) pos[e] = 0;
     __syncwarp();
     const unsigned below = (1u << lane) - 1u;
-    for (int i = lo; i < hi; i += 32) {
-        const int e = i + lane < hi ? idx[i + lane] : -1;
-        const unsigned same = __match_any_sync(kFull, e);
-        if (e >= 0 && (same & below) == 0) pos[e] += __popc(same);
-        __syncwarp();
+    // four steps' indices are read at once
+    constexpr int N = 4;
+    int e[N];
+    auto read = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) e[j] = i + 32 * j + lane < hi ? idx[i + 32 * j + lane] : -1;
+    };
+    for (int i = lo; i < hi; i += 32 * N) {
+        read(i);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const unsigned same = __match_any_sync(kFull, e[j]);
+            if (e[j] >= 0 && (same & below) == 0) pos[e[j]] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += WARPS * 32) {
@@ -727,14 +737,17 @@ __device__ __forceinline__ void scatter_pairs(const int* idx, int n, int32_t p0,
         }
     }
     __syncthreads();
-    for (int i = lo; i < hi; i += 32) {
-        const int e = i + lane < hi ? idx[i + lane] : -1;
-        const unsigned same = __match_any_sync(kFull, e);
-        const int at = e >= 0 ? pos[e] : 0;
-        if (e >= 0) perm[at + __popc(same & below)] = p0 + i + lane;
-        __syncwarp();
-        if (e >= 0 && (same & below) == 0) pos[e] = at + __popc(same);
-        __syncwarp();
+    for (int i = lo; i < hi; i += 32 * N) {
+        if (hi - lo > 32 * N) read(i);  // else they are still here
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const unsigned same = __match_any_sync(kFull, e[j]);
+            const int at = e[j] >= 0 ? pos[e[j]] : 0;
+            if (e[j] >= 0) perm[at + __popc(same & below)] = p0 + i + 32 * j + lane;
+            __syncwarp();
+            if (e[j] >= 0 && (same & below) == 0) pos[e[j]] = at + __popc(same);
+            __syncwarp();
+        }
     }
 }
 

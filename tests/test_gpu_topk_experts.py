@@ -180,9 +180,10 @@ def test_backward(T, E, K, H):
             _check_bwd(_bwd(x, W, bias, g, routing, w), o, routing, K, H)
 
 
-@pytest.mark.parametrize("T,E,K,H,skew", [(40000, 8, 2, 256, 1.0), (30000, 3, 2, 128, 0.3), (4000, 32, 4, 1024, 2.0),
+@pytest.mark.parametrize("T,E,K,H,skew", [(60000, 8, 2, 256, 1.0), (49151, 8, 2, 256, 0.5), (30000, 3, 2, 128, 0.3), (4000, 32, 4, 1024, 2.0),
                                           (20001, 60, 6, 64, 1.0), (6000, 2, 1, 512, 4.0),
-                                          (20000, 4, 2, 192, 1.5), (9001, 2, 2, 256, 0.0), (70000, 9, 2, 128, 0.5)])
+                                          (50000, 4, 2, 192, 1.5), (49152, 2, 2, 256, 0.0), (70000, 9, 2, 128, 0.5),
+                                          (60001, 12, 2, 64, 2.0)])
 def test_many_pairs_and_uneven_experts(T, E, K, H, skew):
     """Several tiles per block, experts cut into pieces and whole ones, experts without a pair."""
     x, W, b, g = _data(T, E, K, H, BF16)
@@ -207,7 +208,7 @@ def _small_integers(T, E, K, H, seed):
 
 
 @pytest.mark.parametrize("T,E,K,H", [(200, 4, 2, 128), (333, 6, 3, 256), (50, 5, 1, 64), (150, 3, 2, 320), (100, 4, 4, 1024),
-                                     (7001, 3, 2, 192), (6000, 2, 2, 256), (9000, 4, 2, 64)])
+                                     (50001, 3, 2, 192), (49152, 2, 2, 256), (52000, 4, 2, 64)])
 def test_exact_on_small_integers(T, E, K, H):
     x, W, b, g, w = _small_integers(T, E, K, H, T)
     routing, _ = _routing(T, E, K, T)
@@ -240,7 +241,7 @@ def _routing_of(idx, E):
                        torch.sort(flat, stable=True)[1].to(i))
 
 
-@pytest.mark.parametrize("T,E,H", [(400, 6, 64), (400, 6, 256), (20000, 6, 256), (15000, 7, 192)])
+@pytest.mark.parametrize("T,E,H", [(400, 6, 64), (400, 6, 256), (50000, 6, 256), (49200, 7, 192)])
 def test_everything_on_one_expert_and_the_same_expert_twice(T, E, H):
     """The larger ones group their tokens by pairs of experts."""
     K = 2
@@ -259,7 +260,7 @@ def test_everything_on_one_expert_and_the_same_expert_twice(T, E, H):
 
 def test_expert_indices_off_eight_bytes():
     """Pairs of indices are read together only where they start on 8 bytes."""
-    T, E, K, H = 20000, 4, 2, 128
+    T, E, K, H = 50000, 4, 2, 128
     x, W, b, g = _data(T, E, K, H, BF16)
     routing, w = _routing(T, E, K)
     off = torch.empty(T * K + 1, dtype=torch.int32, device="cuda")[1:]
@@ -309,7 +310,7 @@ def test_no_tokens():
     assert not dW.any() and not db.any()
 
 
-@pytest.mark.parametrize("T,E,K,H", [(9000, 8, 3, 256), (30000, 5, 2, 256)])
+@pytest.mark.parametrize("T,E,K,H", [(9000, 8, 3, 256), (50000, 5, 2, 256)])
 def test_repeats_bit_for_bit_with_one_workspace(T, E, K, H):
     """Whatever the order in which a token's rows come in: the same bits, call after call, and with
     another size through the same workspace in between; on another stream; captured and replayed."""
