@@ -904,20 +904,21 @@ topk_route_bwd_kernel(const T* __restrict__ logits, int64_t ld, int64_t T_, bool
             if (m == -INFINITY) m = 0.0f;
             for (int k = sub; k < R.K; k += LPT) {
                 pair(k, e, g);
-                if (e >= 0) {
-                    const float p = unnormalised(to_f(row[e]));
-                    z += p;
-                    dot += p * g;
-                }
+                if (e >= 0) z += unnormalised(to_f(row[e]));
             }
             z = lanes_sum<LPT>(z);
+            if (z == 0.0f) z = 1.0f;
+            // the weights are quotients: a weight of 1 is exactly 1, and its gradient exactly 0
+            for (int k = sub; k < R.K; k += LPT) {
+                pair(k, e, g);
+                if (e >= 0) dot += unnormalised(to_f(row[e])) / z * g;
+            }
             dot = lanes_sum<LPT>(dot);
-            const float inv = 1.0f / (z == 0.0f ? 1.0f : z);
             for (int k = sub; k < R.K; k += LPT) {
                 pair(k, e, g);
                 if (e >= 0) {
                     const float x = to_f(row[e]);
-                    float d = unnormalised(x) * inv * (g - dot * inv);
+                    float d = unnormalised(x) / z * (g - dot);
                     if (R.sigmoid) d /= 1.0f + expf(x);
                     row_d[e] = d;
                 }

@@ -377,6 +377,19 @@ def test_gradient_against_differences(rule):
             assert abs((at[0] - at[1]) / (2 * h) - d[t, e].item()) <= 3e-3
 
 
+@pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [1, 8, 40, 256])
+def test_one_renormalised_expert_has_no_gradient(score, E):
+    """Its weight is the scale whatever the logits: the gradient is exactly 0."""
+    rule = R(E, 1, score, True, 2.5)
+    logits, _ = _logits(500, E, F32, 8)
+    got, routing = _run(logits, rule)
+    assert (got["weights"] == 2.5).all()
+    d = torch.ones_like(logits)
+    ops.moe_topk_route_bwd(logits, rule, routing.expert_idx, torch.randn(500, 1, device="cuda"), d)
+    assert not d.any()
+
+
 def test_gradient_leaves_out_experts_outside_the_row():
     rule = R(8, 2, SOFT, True)
     logits, _ = _logits(3, 8, F32, 3)
