@@ -29,7 +29,6 @@
 //     pairs.
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 
 #include "checks.h"
 #include "common.cuh"
@@ -538,10 +537,16 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                         float m = 0.0f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[j]));
+                        if (m == INFINITY) {  // an infinite sum keeps its finite neighbours' bits
+                            m = 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) m = fabsf(v[j]) < INFINITY ? fmaxf(m, fabsf(v[j])) : m;
+                        }
                         // exponent of the largest |v w|, 40 at least: fp16's last step is then 2^-125
                         const int ex = max(static_cast<int>((__float_as_uint(m * fabsf(w)) >> 23) & 255), 40);
                         f = w * __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
-                        f = fminf(fmaxf(f, -3e38f), 3e38f);  // only where |v w| is below 2^-87
+                        // only where |v w| is below 2^-87; an infinite or NaN weight stays what it is
+                        if (fabsf(w) < INFINITY) f = fminf(fmaxf(f, -3e38f), 3e38f);
                         inv[i] = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
                     }
 #pragma unroll
@@ -1513,9 +1518,8 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                     lphase ^= 1;
                 }
             }
-            if (!ok) break;
             if (add) {
-                // the eight warps' sums, in order
+                // the eight warps' sums, in order (warps that gave up come here too: the barrier counts them)
                 asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ctl->db[warp][lane][j] = db[j];
@@ -1534,7 +1538,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                     }
                 }
             }
-            if (!mbar_wait(&ctl->tfull, acc_phase, abort, A.flags)) break;
+            if (!ok || !(ok = mbar_wait(&ctl->tfull, acc_phase, abort, A.flags))) continue;
             __syncwarp();
             tc_fence_after();
             for (int mh = 0; mh < (rows + 127) / 128 && dW; ++mh) {
@@ -1662,45 +1666,16 @@ __global__ void __launch_bounds__(256) wgrad_sum_kernel(const WgradArgs A) {
 }
 
 // ---------------------------------------------------------------- launches
-// The tensor map of a weight array depends on the arguments alone; the last ones are kept,
-// so a layer's calls encode its map once.
-struct MapKey {
-    const void* W;
-    moe_dtype_t dtype;
-    uint64_t rows, cols;
-    uint32_t box_rows;
-    bool operator==(const MapKey& o) const {
-        return W == o.W && dtype == o.dtype && rows == o.rows && cols == o.cols && box_rows == o.box_rows;
-    }
-};
-constexpr int kMaps = 16;
-MapKey g_map_key[kMaps];
-CUtensorMap g_map[kMaps];
-int g_maps = 0, g_map_next = 0;
-std::mutex g_map_mu;
-
 bool weight_map(CUtensorMap* map, const void* W, moe_dtype_t dtype, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-    const MapKey key{W, dtype, rows, cols, box_rows};
-    std::lock_guard<std::mutex> lock(g_map_mu);
-    for (int i = 0; i < g_maps; ++i)
-        if (g_map_key[i] == key) {
-            *map = g_map[i];
-            return true;
-        }
     EncodeTiledFn enc = get_encode_tiled();
     if (!enc) return false;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols * 2};
     const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    if (enc(map, dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-            const_cast<void*>(W), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
-    const int at = g_maps < kMaps ? g_maps++ : g_map_next++ % kMaps;
-    g_map_key[at] = key;
-    g_map[at] = *map;
-    return true;
+    return enc(map, dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+               const_cast<void*>(W), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int BN, bool DX>

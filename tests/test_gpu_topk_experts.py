@@ -297,6 +297,36 @@ def test_a_token_with_nan_leaves_the_others_alone():
     assert torch.isnan(y[17]).all() and not torch.isfinite(y[200]).any()
 
 
+@pytest.mark.parametrize("K", [1, 2, 4])
+def test_an_infinite_weight_of_the_product_leaves_other_columns_alone(K):
+    T, E, H = 300, 4, 128
+    x, W, b, g = _data(T, E, K, H, BF16)
+    routing, w = _routing(T, E, K)
+    o = _reference(x, W, b, g, routing.expert_idx, w)
+    bad = W.clone()
+    bad[2, 7, 5] = float("inf")
+    chosen = (routing.expert_idx.view(T, K) == 2).any(1)
+    assert chosen.any() and (x[:, 5] != 0).all() and (g[:, 7] != 0).all()
+    for name, col, got in (("y", 7, _fwd(x, bad, b, routing, w)), ("d_x", 5, _bwd(x, bad, b, g, routing, w)["d_x"])):
+        assert torch.equal(torch.isinf(got[:, col]), chosen), name
+        got[:, col] = o[name][:, col].to(BF16)
+        _check_rows(name, got, o, K, H)
+
+
+@pytest.mark.parametrize("T,K", [(300, 1), (300, 2), (300, 5), (50000, 2)])
+def test_weights_that_are_nan_or_infinite(T, K):
+    E, H = 6, 128
+    x, W, b, g = _data(T, E, K, H, BF16)
+    routing, w = _routing(T, E, K)
+    good = _fwd(x, W, b, routing, w), _bwd(x, W, b, g, routing, w, ("d_x",))["d_x"]
+    bad = w.clone()
+    bad[3, K - 1], bad[200, 0] = float("nan"), float("inf")
+    rows = torch.tensor([t not in (3, 200) for t in range(T)], device="cuda")
+    for want, got in zip(good, (_fwd(x, W, b, routing, bad), _bwd(x, W, b, g, routing, bad, ("d_x",))["d_x"])):
+        assert torch.equal(got[rows], want[rows])
+        assert torch.isnan(got[3]).all() and not torch.isfinite(got[200]).any()
+
+
 def test_no_tokens():
     E, K, H = 4, 2, 128
     _, W, b, _ = _data(1, E, K, H, BF16)
