@@ -126,11 +126,15 @@ __device__ __forceinline__ void load_logits(const T* row, int e0, int E, bool ve
 }
 
 // The bias of a lane's experts, NaN past the last one: what is no expert is then NaN in
-// every value that is compared.
+// every value that is compared. A NaN of the caller's masks its expert like a NaN logit.
 template <int VPL>
 __device__ __forceinline__ void load_bias(const float* bias, int e0, int E, float (&b)[VPL]) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) b[j] = e0 + j >= E ? __int_as_float(0x7fffffff) : bias ? bias[e0 + j] : 0.0f;
+    for (int j = 0; j < VPL; ++j) {
+        b[j] = e0 + j < E && bias ? bias[e0 + j] : 0.0f;
+        if (b[j] != b[j]) b[j] = -INFINITY;
+        if (e0 + j >= E) b[j] = __int_as_float(0x7fffffff);
+    }
 }
 
 __device__ __forceinline__ bool is_masked(float l) { return !(l > -INFINITY); }

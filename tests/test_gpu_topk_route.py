@@ -212,6 +212,21 @@ def test_nan_is_never_chosen_over_a_number():
     assert np.isfinite(got["weights"][[0, 1, 3, 4]]).all() and np.isnan(got["weights"][2]).all()
 
 
+@pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [8, 40, 100, 256])
+@pytest.mark.parametrize("T", [5, 3000])
+def test_a_nan_in_the_bias_masks_its_expert(T, E, score):
+    logits, bias = _logits(T, E, F32, 9)
+    bias[3] = float("nan")
+    got, _ = _run(logits, R(E, E, score) if E == 8 else R(E, 4, score), bias)
+    idx = got["expert_idx"].reshape(T, -1)
+    if E == 8:  # all are chosen, the masked one last
+        assert (idx[:, -1] == 3).all()
+    else:
+        assert (idx != 3).all()
+    assert ((idx >= 0) & (idx < E)).all()
+
+
 def test_weights_stay_finite_where_scores_underflow():
     logits = torch.full((3, 16), -300.0, device="cuda")
     logits[0, 3], logits[1, 5], logits[2, 0] = -250.0, -299.5, 900.0
