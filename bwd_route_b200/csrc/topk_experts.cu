@@ -1693,12 +1693,19 @@ cudaError_t pair_launch(const void* W, moe_dtype_t dtype, const PairArgs& a, int
     return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kPairThreads), C::SMEM_BYTES, s, map, a);
 }
 
-// Columns per tile: 256 where that leaves a tile for every SM, narrower ones for few pairs.
+// Columns per tile: the width whose tiles take the SMs the least time. A tile of 64, 128 or
+// 256 columns takes about 10, 11 or 18 (the two halves of the wider ones drain at once, the
+// gather is the same), and the tiles go around in whole turns. Forward and backward, K = 2:
+// 5003 tokens, E 4, H 128: 64 columns 28.0 us, 128: 25.8; 4,000, E 8, H 256: 41.2 / 39.2,
+// 256: 41.1; 2,500, E 16, H 1024: 78.6 / 73.4 / 77.3; 30,000, E 8, H 256: 98.7 / 84.8 / 84.3.
 int tile_columns(int64_t P, int E, int H, int sms) {
-    const int64_t m = P / 128 + (P < E ? P : E);
-    if (H > 128 && m * ((H + 255) / 256) >= sms) return 256;
-    if (H > 64 && m * ((H + 127) / 128) >= sms) return 128;
-    return 64;
+    const int64_t hit = P < E ? P : E, some = P / 128 + hit / 2, rows = some > hit ? some : hit;  // of 128 pairs, about
+    auto time = [&](int bn, int each) { return (rows * ((H + bn - 1) / bn) + sms - 1) / sms * each; };
+    int best = 64;
+    int64_t least = time(64, 10);
+    if (H > 64 && time(128, 11) < least) least = time(128, 11), best = 128;
+    if (H > 128 && time(256, 18) < least) best = 256;
+    return best;
 }
 
 template <typename T, bool DX>
@@ -1799,7 +1806,8 @@ cudaError_t wgrad_launch(const WgradArgs& a, int sms, cudaStream_t s) {
     const int64_t units = (hit + a.extra) * wgrad_tiles(a.H);
     e = launch_pdl(wgrad_kernel<T>, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kWThreads), kWSmem, s, a);
     if (e != cudaSuccess) return e;
-    int x = a.H * a.H / 256;
+    // one turn of a block's loop up to H = 128 (5003 tokens, H 128: the whole backward 29.5 -> 28.0 us)
+    int x = a.H * a.H / 128;
     if (x > 256) x = 256;
     return launch_pdl(wgrad_sum_kernel<T>, dim3(x, a.E), dim3(256), 0, s, a);
 }
