@@ -703,17 +703,16 @@ __device__ __forceinline__ int exclusive_scan_256(int v, int* s_warp) {
 }
 
 // Writes perm for the n pairs idx[0..n) whose first pair has number p0: the next position
-// of expert e is s_base[e]. s_pos: [warps][E]. Pairs of one expert stay in order: a warp
-// has a run of consecutive pairs, lanes of one expert are ranked by __match_any_sync.
-template <int WARPS>
+// of expert e is s_base[e], which the whole block fills in bases() once its pairs are
+// counted. s_pos: [warps][E]. Pairs of one expert stay in order: a warp has a run of
+// consecutive pairs, lanes of one expert are ranked by __match_any_sync.
+template <int WARPS, typename F>
 __device__ __forceinline__ void scatter_pairs(const int* idx, int n, int32_t p0, int E, const int* s_base, int* s_pos,
-                                              int32_t* __restrict__ perm) {
+                                              int32_t* __restrict__ perm, F bases) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int run = ((n + WARPS - 1) / WARPS + 31) & ~31;
     const int lo = min(n, warp * run), hi = min(n, lo + run);
     int* pos = s_pos + warp * E;
-    for (int e = lane; e < E; e += 32) pos[e] = 0;
-    __syncwarp();
     const unsigned below = (1u << lane) - 1u;
     // four steps' indices are read at once
     constexpr int N = 4;
@@ -722,8 +721,11 @@ __device__ __forceinline__ void scatter_pairs(const int* idx, int n, int32_t p0,
 #pragma unroll
         for (int j = 0; j < N; ++j) e[j] = i + 32 * j + lane < hi ? idx[i + 32 * j + lane] : -1;
     };
+    read(lo);
+    for (int i = lane; i < E; i += 32) pos[i] = 0;
+    __syncwarp();
     for (int i = lo; i < hi; i += 32 * N) {
-        read(i);
+        if (i != lo) read(i);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const unsigned same = __match_any_sync(kFull, e[j]);
@@ -731,6 +733,7 @@ __device__ __forceinline__ void scatter_pairs(const int* idx, int n, int32_t p0,
             __syncwarp();
         }
     }
+    bases();
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += WARPS * 32) {
         int at = s_base[e];
@@ -809,7 +812,7 @@ topk_route_small_kernel(const T* __restrict__ logits, int64_t ld, int T_, bool v
     }
     if (e == 0) offsets[R.E] = T_ * R.K;
     __syncthreads();
-    scatter_pairs<WARPS>(s_idx, T_ * R.K, 0, R.E, s_base, reinterpret_cast<int*>(areas), perm);
+    scatter_pairs<WARPS>(s_idx, T_ * R.K, 0, R.E, s_base, reinterpret_cast<int*>(areas), perm, [] {});
 }
 
 // 32 experts a block (a lane each), the routing blocks in 32 runs (a warp each): sums of
@@ -820,21 +823,22 @@ __global__ void __launch_bounds__(1024) topk_scan_kernel(const int32_t* __restri
     __shared__ int s_run[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
     const int run = (nblk + 31) / 32, lo = warp * run, hi = min(nblk, lo + run);
-    int sum = 0;
-    if (e < E) {
-#pragma unroll 8
-        for (int b = lo; b < hi; ++b) sum += blk_counts[static_cast<int64_t>(b) * E + e];
+    constexpr int N = kMaxBlocks / 32;  // blocks of a run at most; their counts stay in registers
+    int c[N], sum = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        c[i] = lo + i < hi && e < E ? blk_counts[static_cast<int64_t>(lo + i) * E + e] : 0;
+        sum += c[i];
     }
     s_run[warp][lane] = sum;
     __syncthreads();
     int at = 0;
     for (int w = 0; w < warp; ++w) at += s_run[w][lane];
     if (e < E) {
-#pragma unroll 8
-        for (int b = lo; b < hi; ++b) {
-            const int c = blk_counts[static_cast<int64_t>(b) * E + e];
-            blk_base[static_cast<int64_t>(b) * E + e] = at;
-            at += c;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (lo + i < hi) blk_base[static_cast<int64_t>(lo + i) * E + e] = at;
+            at += c[i];
         }
         if (warp == 31) counts[e] = at;
     }
@@ -849,16 +853,19 @@ topk_scatter_kernel(const int32_t* __restrict__ expert_idx, int64_t pairs, int p
     __shared__ int s_warp[32];
     __shared__ int s_base[kMaxE];
     const int e = threadIdx.x;
-    const int off = exclusive_scan_256(e < E ? counts[e] : 0, s_warp);
-    if (e < E) {
-        s_base[e] = off + blk_base[static_cast<int64_t>(blockIdx.x) * E + e];
-        if (blockIdx.x == 0) offsets[e] = off;
-    }
+    // on the way while the pairs are counted
+    const int count = e < E ? counts[e] : 0;
+    const int before = e < E ? blk_base[static_cast<int64_t>(blockIdx.x) * E + e] : 0;
     if (blockIdx.x == 0 && e == 0) offsets[E] = static_cast<int32_t>(pairs);
-    __syncthreads();
     const int64_t p0 = static_cast<int64_t>(blockIdx.x) * ppb;
     const int n = static_cast<int>(pairs - p0 < ppb ? pairs - p0 : ppb);
-    scatter_pairs<kWarps>(expert_idx + p0, n, static_cast<int32_t>(p0), E, s_base, reinterpret_cast<int*>(smem), perm);
+    scatter_pairs<kWarps>(expert_idx + p0, n, static_cast<int32_t>(p0), E, s_base, reinterpret_cast<int*>(smem), perm, [&] {
+        const int off = exclusive_scan_256(count, s_warp);
+        if (e < E) {
+            s_base[e] = off + before;
+            if (blockIdx.x == 0) offsets[e] = off;
+        }
+    });
 }
 
 // Gradient of the logits: a token per LPT lanes, its row of gradients built in shared
