@@ -9,7 +9,9 @@
 // `wpr` warps (the fewest that hold it at 16 values a thread); the other warps of
 // the block have rows of their own, and the block walks over the rows with the next
 // row's loads in flight, so gamma, beta and (backward) the thread's column sums stay
-// in registers.
+// in registers. 1,048,576 x 256 fp32 forward: 368 us, 5.8 TB/s (a copy: 6.55). 262,144 x
+// 256 fp32 backward: 132 us, 6.1 TB/s, and 3 us for the second kernel. One row of 1024
+// bf16: 2.9 us on the device.
 //
 // dgamma and dbeta: a thread always sees the same columns, so it adds up its rows in
 // registers; every kFlush rows it adds that to its shared-memory sums (two levels, so
@@ -142,6 +144,9 @@ norm_fwd_kernel(const T* x, int64_t ldx, const P* __restrict__ gamma, const P* _
 }
 
 // part: [gridDim.x][2][H] column sums of the block's rows (dgamma, dbeta), or NULL.
+// One row team's chain (loads, two sums over the team, stores) is long where H is odd and
+// values come one by one: 4099 x 1001 fp16 17 us, bound by that chain, not by its 25 MB.
+// Two or four rows a team at once were slower (19.6, 24.8 us): fewer teams run.
 template <typename T, typename P, int VEC, int N, int BLOCK>
 __global__ void __launch_bounds__(BLOCK)
 norm_bwd_kernel(const T* __restrict__ x, const T* dy, int64_t ldx, const P* __restrict__ gamma,
