@@ -5,13 +5,14 @@
 //   dgamma = sum_t dy n,   dbeta = sum_t dy
 //
 // Bound: HBM. Both directions are one pass: a row is read once into registers, its
-// sums are taken from there, and the result is written from there. A row belongs to
-// `wpr` warps (the fewest that hold it at 16 values a thread); the other warps of
-// the block have rows of their own, and the block walks over the rows with the next
-// row's loads in flight, so gamma, beta and (backward) the thread's column sums stay
-// in registers. 1,048,576 x 256 fp32 forward: 368 us, 5.8 TB/s (a copy: 6.55). 262,144 x
-// 256 fp32 backward: 132 us, 6.1 TB/s, and 3 us for the second kernel. One row of 1024
-// bf16: 2.9 us on the device.
+// sums are taken from there, and the result is written from there. A row belongs to 4 to
+// 512 threads (values_per_thread); the block's other threads have rows of their own, and
+// the block walks over the rows with the next row's loads in flight, so gamma, beta and
+// (backward) the thread's column sums stay in registers. Loads are 16 bytes wide where every
+// row starts on 16, else two values, else one. 1,048,576 x 256 fp32 forward: 335 to 368 us,
+// 5.8 to 6.4 TB/s (a copy: 6.55). 262,144 x 256 fp32 backward: 120 to 132 us, 6.1 TB/s or more, and 3 to 4 us for the
+// second kernel. One row of 1024 bf16: 2.9 us on the device. 524,288 x 16 fp16 forward, a
+// row for every four threads: 17 us (a warp for a row: 111).
 //
 // dgamma and dbeta: a thread always sees the same columns, so it adds up its rows in
 // registers; every kFlush rows it adds that to its shared-memory sums (two levels, so
@@ -37,15 +38,17 @@ constexpr int kPerThread = 16;    // values of a row a thread holds at most
 constexpr int kFlush = 64;        // rows between two flushes of the column sums
 constexpr int kMaxBlocks = 1024;  // partial-sum rows the workspace holds
 
-// Sum over the wpr warps of a row; every thread of the block calls it.
+// Sum over the tpr threads of a row; every thread of the block calls it.
 template <int V>
-__device__ __forceinline__ void team_sum(float (&v)[V], float (*red)[16], int wpr) {
+__device__ __forceinline__ void team_sum(float (&v)[V], float (*red)[16], int tpr) {
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1)
+    for (int off = 16; off >= 1; off >>= 1) {
+        if (off >= tpr) continue;
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-    if (wpr == 1) return;
-    const int warp = threadIdx.x >> 5;
+    }
+    if (tpr <= 32) return;
+    const int warp = threadIdx.x >> 5, wpr = tpr >> 5;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
         for (int i = 0; i < V; ++i) red[i][warp] = v[i];
@@ -85,10 +88,11 @@ __device__ __forceinline__ void load_row(const T* row, int tpr, int r, int H, bo
 template <typename T, typename P, int VEC, int N, int BLOCK>
 __global__ void __launch_bounds__(BLOCK)
 norm_fwd_kernel(const T* x, int64_t ldx, const P* __restrict__ gamma, const P* __restrict__ beta, float eps, T* y,
-                float* __restrict__ mean, float* __restrict__ rstd, int64_t T_, int H, int wpr) {
+                float* __restrict__ mean, float* __restrict__ rstd, int64_t T_, int H, int tpr_) {
     griddep_wait();  // every global access below comes after the previous grid
     __shared__ float s_red[2][1][16];
-    const int tpr = 32 * wpr, team = threadIdx.x / tpr, r = threadIdx.x % tpr, teams = BLOCK / tpr;
+    const int tpr = BLOCK == 512 ? 512 : tpr_;
+    const int team = threadIdx.x / tpr, r = threadIdx.x % tpr, teams = BLOCK / tpr;
     const float h = static_cast<float>(H);
     float g[N * VEC], b[N * VEC];
     load_params<P, VEC, N>(gamma, 1.0f, tpr, r, H, g);
@@ -111,7 +115,7 @@ norm_fwd_kernel(const T* x, int64_t ldx, const P* __restrict__ gamma, const P* _
             }
         }
         load_row<T, VEC, N>(x + (row + step) * ldx, tpr, r, H, row + step < T_, next);
-        team_sum(s, s_red[0], wpr);
+        team_sum(s, s_red[0], tpr);
         const float mu = s[0] / h;
         s[0] = 0.0f;
 #pragma unroll
@@ -123,7 +127,7 @@ norm_fwd_kernel(const T* x, int64_t ldx, const P* __restrict__ gamma, const P* _
                 if (on) s[0] += v[j * VEC + i] * v[j * VEC + i];
             }
         }
-        team_sum(s, s_red[1], wpr);
+        team_sum(s, s_red[1], tpr);
         const float rs = rsqrtf(s[0] / h + eps);
         if (!valid) continue;
         T* out = y + row * H;
@@ -145,17 +149,17 @@ norm_fwd_kernel(const T* x, int64_t ldx, const P* __restrict__ gamma, const P* _
 
 // part: [gridDim.x][2][H] column sums of the block's rows (dgamma, dbeta), or NULL.
 // One row team's chain (loads, two sums over the team, stores) is long where H is odd and
-// values come one by one: 4099 x 1001 fp16 17 us, bound by that chain, not by its 25 MB.
-// Two or four rows a team at once were slower (19.6, 24.8 us): fewer teams run.
+// values come one by one; two or four rows a team at once were slower: fewer teams run.
 template <typename T, typename P, int VEC, int N, int BLOCK>
 __global__ void __launch_bounds__(BLOCK)
 norm_bwd_kernel(const T* __restrict__ x, const T* dy, int64_t ldx, const P* __restrict__ gamma,
                 const float* __restrict__ mean, const float* __restrict__ rstd, T* dx, float* __restrict__ part,
-                int64_t T_, int H, int wpr) {
+                int64_t T_, int H, int tpr_) {
     griddep_wait();  // every global access below comes after the previous grid
     extern __shared__ float s_sum[];  // [2][N * VEC][BLOCK], each thread its own
     __shared__ float s_red[2][2][16];
-    const int tpr = 32 * wpr, team = threadIdx.x / tpr, r = threadIdx.x % tpr, teams = BLOCK / tpr;
+    const int tpr = BLOCK == 512 ? 512 : tpr_;
+    const int team = threadIdx.x / tpr, r = threadIdx.x % tpr, teams = BLOCK / tpr;
     const float inv_h = 1.0f / static_cast<float>(H);
     constexpr int EPT = N * VEC;
     float g[EPT], ag[EPT], ab[EPT];
@@ -200,7 +204,7 @@ norm_bwd_kernel(const T* __restrict__ x, const T* dy, int64_t ldx, const P* __re
         }
         fetch(row + step);
         if (dx) {
-            team_sum(s, s_red[phase], wpr);
+            team_sum(s, s_red[phase], tpr);
             phase ^= 1;
             const float c1 = s[0] * inv_h, c2 = s[1] * inv_h;
             if (valid) {
@@ -275,14 +279,21 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
     }
 }
 
-// Warps per row: the fewest powers of two that hold H at kPerThread values a thread; at
-// four where they come one by one and a block of 256 threads holds the row (4099 x 1001
-// fp16 backward: 16.6 us against 21.8 at 16 single values a thread).
-int warps_per_row(int H, bool vec) {
-    const int per = vec || H > 1024 ? kPerThread : 4;
-    int w = 1;
-    while (w * 32 * per < H) w *= 2;
-    return w;
+// Threads per row: the fewest powers of two that hold H at `per` values a thread.
+int threads_per_row(int H, int per) {
+    int t = 4;
+    while (t * per < H) t *= 2;
+    return t;
+}
+
+// Values of a row a thread holds, for chunks of `width` (V: 16 bytes). More of them make fewer
+// threads of a row and shorter sums, fewer a lighter loop. Backward, 8 / 16 a thread: 64,035 x 131
+// fp16 39 / 57 us, 32,513 x 258 41 / 50, 8,371 x 1002 27 / 37; forward 30 / 38, 27 / 23, 16 / 18.
+// Whole 16-byte chunks of 16-bit values (65,536 x 128): 15 / 14, forward 10 / 9; fp32 20 / 21,
+// 10 / 10, and 22 / 21, 13 / 10 at 16,384 x 512, where 8 a thread leave the warp.
+int values_per_thread(int H, int width, int V) {
+    if (H > 2048 && width != V) return kPerThread;
+    return width == V && (V == 8 || H > 256) ? kPerThread : 8;
 }
 
 // Blocks: enough for every row team to have a row, at most what runs at once
@@ -341,22 +352,22 @@ struct BwdArgs {
 };
 
 template <typename T, typename P, int VEC, int N, int BLOCK>
-cudaError_t fwd_launch(const FwdArgs& a, int wpr, cudaStream_t s) {
+cudaError_t fwd_launch(const FwdArgs& a, int tpr, cudaStream_t s) {
     auto kernel = norm_fwd_kernel<T, P, VEC, N, BLOCK>;
-    const int teams = BLOCK / (32 * wpr);
+    const int teams = BLOCK / tpr;
     static Resident known;
     int grid = 0;
     cudaError_t e = persistent_grid(kernel, known, BLOCK, 0, (a.T + teams - 1) / teams, &grid);
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(grid), dim3(BLOCK), 0, s, static_cast<const T*>(a.x), a.ldx,
                       static_cast<const P*>(a.gamma), static_cast<const P*>(a.beta), a.eps, static_cast<T*>(a.y), a.mean,
-                      a.rstd, a.T, a.H, wpr);
+                      a.rstd, a.T, a.H, tpr);
 }
 
 template <typename T, typename P, int VEC, int N, int BLOCK>
-cudaError_t bwd_launch(const BwdArgs& a, int wpr, cudaStream_t s) {
+cudaError_t bwd_launch(const BwdArgs& a, int tpr, cudaStream_t s) {
     auto kernel = norm_bwd_kernel<T, P, VEC, N, BLOCK>;
-    const int teams = BLOCK / (32 * wpr);
+    const int teams = BLOCK / tpr;
     const size_t smem = sizeof(float) * 2 * N * VEC * BLOCK;
     static Resident known;
     int grid = 0;
@@ -370,7 +381,7 @@ cudaError_t bwd_launch(const BwdArgs& a, int wpr, cudaStream_t s) {
     e = persistent_grid(kernel, known, BLOCK, smem, want, &grid);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(grid), dim3(BLOCK), smem, s, static_cast<const T*>(a.x), static_cast<const T*>(a.dy),
-                   a.ldx, static_cast<const P*>(a.gamma), a.mean, a.rstd, static_cast<T*>(a.dx), a.part, a.T, a.H, wpr);
+                   a.ldx, static_cast<const P*>(a.gamma), a.mean, a.rstd, static_cast<T*>(a.dx), a.part, a.T, a.H, tpr);
     if (e != cudaSuccess || !a.part) return e;
     return launch_pdl(norm_reduce_kernel<P>, dim3((a.H + 31) / 32, 2), dim3(32, 32), 0, s,
                       static_cast<const float*>(a.part), grid, a.H, static_cast<P*>(a.dgamma), static_cast<P*>(a.dbeta));
@@ -378,46 +389,59 @@ cudaError_t bwd_launch(const BwdArgs& a, int wpr, cudaStream_t s) {
 
 // Chunk count per thread by row length; above 4096 values a row takes 512 threads.
 template <bool FWD, typename T, typename P, typename A>
-cudaError_t norm_dispatch(const A& a, bool vec, cudaStream_t s) {
+cudaError_t norm_dispatch(const A& a, int width, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    const int wpr = warps_per_row(a.H, vec);
-    const int per = (a.H + 32 * wpr - 1) / (32 * wpr);  // values a thread holds
+    const int tpr = threads_per_row(a.H, values_per_thread(a.H, width, V));
+    const int chunks = (a.H + width * tpr - 1) / (width * tpr);  // of a thread
 #define MOE_NORM(VEC, N, BLOCK)                                       \
     do {                                                              \
-        if constexpr (FWD) return fwd_launch<T, P, VEC, N, BLOCK>(a, wpr, s); \
-        else return bwd_launch<T, P, VEC, N, BLOCK>(a, wpr, s);       \
+        if constexpr (FWD) return fwd_launch<T, P, VEC, N, BLOCK>(a, tpr, s); \
+        else return bwd_launch<T, P, VEC, N, BLOCK>(a, tpr, s);       \
     } while (0)
-    if (vec) {
-        if (wpr > 8) MOE_NORM(V, kPerThread / V, 512);
-        if (per <= V) MOE_NORM(V, 1, 256);
+    if (width == V) {
+        if (tpr > 256) MOE_NORM(V, kPerThread / V, 512);
+        if (chunks == 1) MOE_NORM(V, 1, 256);
         if constexpr (V == 4) {
-            if (per <= 2 * V) MOE_NORM(V, 2, 256);
+            if (chunks == 2) MOE_NORM(V, 2, 256);
         }
         MOE_NORM(V, kPerThread / V, 256);
     }
-    if (wpr > 8) MOE_NORM(1, kPerThread, 512);
-    if (per <= 4) MOE_NORM(1, 4, 256);
+    if (width == 2) {
+        if (tpr > 256) MOE_NORM(2, kPerThread / 2, 512);
+        if (chunks <= 2) MOE_NORM(2, 2, 256);
+        if (chunks <= 4) MOE_NORM(2, 4, 256);
+        MOE_NORM(2, kPerThread / 2, 256);
+    }
+    if (tpr > 256) MOE_NORM(1, kPerThread, 512);
+    if (chunks <= 4) MOE_NORM(1, 4, 256);
+    if (chunks <= 8) MOE_NORM(1, 8, 256);
     MOE_NORM(1, kPerThread, 256);
 #undef MOE_NORM
 }
 
 template <bool FWD, typename A>
-cudaError_t norm_types(const A& a, moe_dtype_t dtype, moe_dtype_t param, bool vec, cudaStream_t s) {
-    if (dtype == MOE_DTYPE_F32) return norm_dispatch<FWD, float, float>(a, vec, s);
+cudaError_t norm_types(const A& a, moe_dtype_t dtype, moe_dtype_t param, int width, cudaStream_t s) {
+    if (dtype == MOE_DTYPE_F32) return norm_dispatch<FWD, float, float>(a, width, s);
     if (dtype == MOE_DTYPE_BF16)
-        return param == MOE_DTYPE_F32 ? norm_dispatch<FWD, __nv_bfloat16, float>(a, vec, s)
-                                      : norm_dispatch<FWD, __nv_bfloat16, __nv_bfloat16>(a, vec, s);
-    return param == MOE_DTYPE_F32 ? norm_dispatch<FWD, __half, float>(a, vec, s)
-                                  : norm_dispatch<FWD, __half, __half>(a, vec, s);
+        return param == MOE_DTYPE_F32 ? norm_dispatch<FWD, __nv_bfloat16, float>(a, width, s)
+                                      : norm_dispatch<FWD, __nv_bfloat16, __nv_bfloat16>(a, width, s);
+    return param == MOE_DTYPE_F32 ? norm_dispatch<FWD, __half, float>(a, width, s)
+                                  : norm_dispatch<FWD, __half, __half>(a, width, s);
 }
 
-// Whole 16-byte chunks: every row and parameter array starts on 16 bytes.
-bool can_vec(moe_dtype_t dtype, int H, int64_t ldx, const void* const* ptrs, int n) {
-    const int v = static_cast<int>(16 / dtype_bytes(dtype));
-    if (H % v != 0 || ldx % v != 0) return false;
-    for (int i = 0; i < n; ++i)
-        if (!aligned(ptrs[i], 16)) return false;
-    return true;
+// Values that are loaded at once: 16 bytes of them where every row and parameter array
+// starts on 16 bytes (a float parameter array's chunk then starts on 16 bytes too), two
+// where they start on two values, else one.
+int chunk_width(moe_dtype_t dtype, int H, int64_t ldx, const void* const* ptrs, int n, moe_dtype_t param,
+                const void* const* params, int np) {
+    for (const int v : {static_cast<int>(16 / dtype_bytes(dtype)), 2}) {
+        bool ok = H % v == 0 && ldx % v == 0;
+        for (int i = 0; i < n; ++i) ok = ok && aligned(ptrs[i], v * dtype_bytes(dtype));
+        const size_t pb = v * dtype_bytes(param);
+        for (int i = 0; i < np; ++i) ok = ok && aligned(params[i], pb < 16 ? pb : 16);
+        if (ok) return v;
+    }
+    return 1;
 }
 
 moe_status_t norm_shape(moe_dtype_t dtype, moe_dtype_t param, int64_t T, int32_t H, int64_t ldx) {
@@ -453,10 +477,10 @@ moe_status_t moe_layer_norm_fwd(const void* x, moe_dtype_t dtype, int64_t T, int
     const Range xr = {x, rows_bytes(T, H, ldx, b)};
     if (any_alias(outs, 3, ins, 2) || any_alias(outs + (in_place ? 1 : 0), in_place ? 2 : 3, &xr, 1)) return MOE_ERR_ALIAS;
     if (T == 0) return MOE_OK;
-    const void* ptrs[4] = {x, y, gamma, beta};
+    const void *ptrs[2] = {x, y}, *params[2] = {gamma, beta};
     const FwdArgs a{x, ldx, gamma, beta, eps, y, mean, rstd, T, H};
-    return cuda_status(
-        norm_types<true>(a, dtype, param_dtype, can_vec(dtype, H, ldx, ptrs, 4), static_cast<cudaStream_t>(stream)));
+    return cuda_status(norm_types<true>(a, dtype, param_dtype, chunk_width(dtype, H, ldx, ptrs, 2, param_dtype, params, 2),
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_layer_norm_workspace_bytes(int64_t T, int32_t H) {
@@ -506,10 +530,10 @@ moe_status_t moe_layer_norm_bwd(const void* x, const void* dy, moe_dtype_t dtype
         if (workspace_bytes < moe_layer_norm_workspace_bytes(T, H)) return MOE_ERR_WORKSPACE;
         part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
     }
-    const void* ptrs[4] = {x, dy, dx, gamma};
+    const void* ptrs[3] = {x, dy, dx};
     const BwdArgs a{x, dy, ldx, gamma, mean, rstd, dx, dgamma, dbeta, part, T, H};
     return cuda_status(
-        norm_types<false>(a, dtype, param_dtype, can_vec(dtype, H, ldx, ptrs, 4), s));
+        norm_types<false>(a, dtype, param_dtype, chunk_width(dtype, H, ldx, ptrs, 3, param_dtype, &gamma, 1), s));
 }
 
 }  // extern "C"

@@ -80,7 +80,9 @@ def _check_y(y, x, gamma, beta, eps):
 
 SHAPES = [(1, 1), (3, 2), (5, 7), (1, 8), (2, 31), (9, 32), (8, 33), (17, 64), (7, 100), (33, 127), (4, 128), (1000, 256),
           (5, 512), (3, 513), (6, 1000), (7, 1001), (2, 1024), (3, 2048), (2, 4096), (2, 4097), (3, 5000), (2, 8191),
-          (2, 8192), (4099, 40)]
+          (2, 8192), (4099, 40),
+          # rows of 4 to 32 threads, odd numbers of them, and widths that allow two values at a time
+          (1001, 16), (30001, 3), (777, 50), (333, 58), (130, 258), (65, 500), (67, 1002), (9, 2050), (5, 7970), (20000, 64)]
 
 
 @pytest.mark.parametrize("dtype,pdtype", [(F32, F32), (BF16, BF16), (F16, F32), (F16, F16), (BF16, F32)], ids=str)
@@ -134,8 +136,9 @@ def _backward(x, gamma, dy, eps, want=("dx", "dgamma", "dbeta"), dx_over_dy=Fals
         ref = r * (u - s1 - n * s2)
         tol = r * (4 * U * (u.abs() + s1.abs() + (n * s2).abs()) + e1 + n.abs() * e2 + dn * s2.abs()) * 1.01
         _within("dx", out["dx"].t, ref, tol + _half(dtype) * (ref.abs() + tol) + _tiny(dtype))
-    # Sums over tokens: at most 64 rows in a register, ceil(T / 64) flushes, 16 row teams, 32 + 32 blocks.
-    chain = (64 + -(-T // 64) + 16 + 64) * U
+    # Sums over tokens: at most 64 rows in a register, ceil(T / 64) flushes, 64 row teams (256 threads,
+    # 4 of them a row at least), 32 + 32 blocks.
+    chain = (64 + -(-T // 64) + 64 + 64) * U
     for k, ref, mag in (("dgamma", (d * n).sum(0), (d.abs() * (n.abs() * chain + dn)).sum(0)),
                         ("dbeta", d.sum(0), d.abs().sum(0) * chain)):
         if k in want:
