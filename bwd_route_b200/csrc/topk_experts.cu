@@ -1236,6 +1236,7 @@ struct WgradArgs {
     void* db;       // may be NULL
     float* part;    // [slots][H][H]
     float* part_db; // [slots][H]
+    int32_t* starts;  // [E + 1]: first slot of each expert, for wgrad_sum_kernel
     uint32_t* flags;
 };
 
@@ -1287,6 +1288,8 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
     if (warp == 0) piece_starts(ctl, A.E, A.P, A.extra);
     __syncthreads();
     const int npieces = ctl->pstart[A.E];  // at most E + extra
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= A.E; e += kWThreads) A.starts[e] = ctl->sstart[e];
     // The pieces by size, largest first: the blocks take units in turns that run back and forth, so
     // that a large unit is followed by a small one. The stages hold the sizes meanwhile.
     int* sizes = reinterpret_cast<int*>(smem);
@@ -1621,28 +1624,41 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
 template <typename T>
 __global__ void __launch_bounds__(256) wgrad_sum_kernel(const WgradArgs A) {
     griddep_wait();  // every global access below comes after the previous grid
-    __shared__ struct {
-        int off[kMaxE + 1], pstart[kMaxE + 1], sstart[kMaxE + 1];
-        float4 sum[256];
-    } s;
+    __shared__ float4 sums[256];
     const int e = blockIdx.y, H = A.H;
-    const int n = A.offsets[e + 1] - A.offsets[e];
-    const int pieces = wgrad_pieces(n, A.P, A.extra);
-    if (pieces == 1) return;
-    int64_t slot = 0;
-    if (pieces > 1) {
-        for (int i = threadIdx.x; i <= A.E; i += 256) s.off[i] = A.offsets[i];
-        __syncthreads();
-        if (threadIdx.x < 32) piece_starts(&s, A.E, A.P, A.extra);
-        __syncthreads();
-        slot = s.sstart[e];
-    }
+    const int64_t slot = A.starts[e];
+    const int pieces = A.starts[e + 1] - static_cast<int>(slot);
+    if (pieces == 0 && A.offsets[e + 1] > A.offsets[e]) return;
     const int64_t nW = static_cast<int64_t>(H) * H;
     // G threads share four elements: each adds pieces g, g + G, ... in order, then the G sums in order
     int G = 1;
-    while (G < 8 && G < pieces) G *= 2;
+    while (G < 8 && pieces > 4 && G < pieces) G *= 2;
     const int per = 256 / G, g = threadIdx.x / per, at = threadIdx.x % per;
     auto add = [&](const float* part, int64_t stride, T* out, int64_t count) {
+        if (pieces <= 4) {  // a thread adds its elements' pieces alone, two of four elements at a time
+            const int64_t step = static_cast<int64_t>(gridDim.x) * 256 * 4;
+            for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < count; i += 2 * step) {
+                float4 v[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[h][j] = j < pieces && i + h * step < count
+                                      ? __ldcg(reinterpret_cast<const float4*>(part + (slot + j) * stride + i + h * step))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (i + h * step >= count) continue;
+                    Chunk<T, 4> o;
+                    o.v[0] = from_f<T>(v[h][0].x + v[h][1].x + v[h][2].x + v[h][3].x);
+                    o.v[1] = from_f<T>(v[h][0].y + v[h][1].y + v[h][2].y + v[h][3].y);
+                    o.v[2] = from_f<T>(v[h][0].z + v[h][1].z + v[h][2].z + v[h][3].z);
+                    o.v[3] = from_f<T>(v[h][0].w + v[h][1].w + v[h][2].w + v[h][3].w);
+                    *reinterpret_cast<Chunk<T, 4>*>(out + i + h * step) = o;
+                }
+            }
+            return;
+        }
         for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * per * 4; i0 < count; i0 += static_cast<int64_t>(gridDim.x) * per * 4) {
             const int64_t i = i0 + at * 4;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1656,11 +1672,11 @@ __global__ void __launch_bounds__(256) wgrad_sum_kernel(const WgradArgs A) {
                     a.w += v.w;
                 }
             }
-            s.sum[threadIdx.x] = a;
+            sums[threadIdx.x] = a;
             __syncthreads();
             if (g == 0 && i < count) {
                 for (int k = 1; k < G; ++k) {
-                    const float4 v = s.sum[k * per + at];
+                    const float4 v = sums[k * per + at];
                     a.x += v.x;
                     a.y += v.y;
                     a.z += v.z;
@@ -1821,9 +1837,10 @@ cudaError_t wgrad_launch(const WgradArgs& a, int sms, cudaStream_t s) {
     const int64_t units = (hit + a.extra) * wgrad_tiles(a.H);
     e = launch_pdl(wgrad_kernel<T>, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kWThreads), kWSmem, s, a);
     if (e != cudaSuccess) return e;
-    // one turn of a block's loop up to H = 128 (5003 tokens, H 128: the whole backward 29.5 -> 28.0 us)
-    int x = a.H * a.H / 128;
-    if (x > 256) x = 256;
+    // 32 blocks an SM for the experts that are cut, each at least 128 elements (of eight pieces)
+    const int cut = a.E < a.extra ? a.E : a.extra, most = a.H * a.H / 128 < 256 ? a.H * a.H / 128 : 256;
+    int x = cut > 0 ? (32 * sms + cut - 1) / cut : most;
+    if (x > most) x = most;
     return launch_pdl(wgrad_sum_kernel<T>, dim3(x, a.E), dim3(256), 0, s, a);
 }
 
@@ -1996,6 +2013,7 @@ moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dt
     g.db = db;
     g.part = reinterpret_cast<float*>(ws + L.part);
     g.part_db = reinterpret_cast<float*>(ws + L.part_db);
+    g.starts = reinterpret_cast<int32_t*>(ws + L.starts);
     g.flags = a.flags;
     return cuda_status(dtype == MOE_DTYPE_BF16
                            ? bwd_type<__nv_bfloat16>(W, bias, dtype, a, g, T, routing->expert_idx, d_weights, sms, s)

@@ -45,6 +45,7 @@ struct ExpertsWs {
     size_t list = 0;     // int32 [T], K = 2: tokens by class
     size_t part = 0;     // float [2 * extra][H][H]
     size_t part_db = 0;  // float [2 * extra][H]
+    size_t starts = 0;   // int32 [E + 1]: first slot of each expert
     size_t total = 0;
 };
 
@@ -65,6 +66,7 @@ inline ExpertsWs experts_ws(int64_t T, int E, int K, int H, size_t begin) {
     L.list = take(K == 2 ? sizeof(int32_t) * T : 0);
     L.part = take(sizeof(float) * slots * H * H);
     L.part_db = take(sizeof(float) * slots * H);
+    L.starts = take(sizeof(int32_t) * (static_cast<size_t>(E) + 1));
     L.total = off;
     return L;
 }
