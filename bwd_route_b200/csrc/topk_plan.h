@@ -21,12 +21,18 @@ inline int wgrad_tiles(int H) {
     const int n = (H + kWTile - 1) / kWTile;
     return n * n;
 }
-// Pieces beyond one per expert that the experts share in proportion to their pairs: with
-// few tiles as many as fill the GPU once; with more tiles than SMs an expert is cut where
-// its tiles alone would take a block longer than an even share of all the work.
-inline int wgrad_extra(int E, int H) {
+// Pieces beyond one per expert that the experts share in proportion to their pairs. With few
+// tiles, as many as fill the GPU once; with several tiles an expert, half as many experts as fill
+// it or more, and pairs enough, as many as fill it twice, since experts of uneven sizes would
+// leave the one turn to the largest; where the experts alone fill it, one is cut where its tiles
+// would take a block longer than an even share of all the work. K = 1 or 2, both kernels, filled
+// once / twice: 25,780 tokens, E 13, H 640: 87 / 64 us; 12,000, E 30, H 512 (648 pairs a piece):
+// 67 / 56; 2,000, E 8, H 1024 (444): 34 / 40; 6,000, E 13, H 640 (375): 35 / 43.
+inline int wgrad_extra(int64_t P, int E, int H) {
     const int tiles = wgrad_tiles(H), fill = kWUnits / tiles;
-    return E * tiles >= kWUnits ? fill : fill - E > 0 ? fill - E : 0;
+    if (E >= fill) return fill;
+    const bool twice = tiles > 1 && 2 * E > fill && P >= 512 * static_cast<int64_t>(fill);
+    return (twice ? 2 : 1) * fill - E;
 }
 // Pieces of an expert with n of the P pairs: at most E + extra in all.
 __host__ __device__ inline int wgrad_pieces(int n, int64_t P, int extra) {
@@ -52,7 +58,7 @@ struct ExpertsWs {
 inline ExpertsWs experts_ws(int64_t T, int E, int K, int H, size_t begin) {
     ExpertsWs L;
     const size_t P = static_cast<size_t>(T) * K, nb = static_cast<size_t>((H + 63) / 64 + 1);
-    const size_t slots = 2 * static_cast<size_t>(wgrad_extra(E, H));
+    const size_t slots = 2 * static_cast<size_t>(wgrad_extra(T * K, E, H));
     size_t off = align_up(begin, 256);
     auto take = [&](size_t bytes) {
         const size_t at = off;

@@ -183,7 +183,7 @@ def test_backward(T, E, K, H):
 @pytest.mark.parametrize("T,E,K,H,skew", [(60000, 8, 2, 256, 1.0), (49151, 8, 2, 256, 0.5), (30000, 3, 2, 128, 0.3), (4000, 32, 4, 1024, 2.0),
                                           (20001, 60, 6, 64, 1.0), (6000, 2, 1, 512, 4.0),
                                           (50000, 4, 2, 192, 1.5), (49152, 2, 2, 256, 0.0), (70000, 9, 2, 128, 0.5),
-                                          (60001, 12, 2, 64, 2.0)])
+                                          (60001, 12, 2, 64, 2.0), (9001, 13, 1, 640, 1.0), (5000, 8, 2, 1024, 1.0)])
 def test_many_pairs_and_uneven_experts(T, E, K, H, skew):
     """Several tiles per block, experts cut into pieces and whole ones, experts without a pair."""
     x, W, b, g = _data(T, E, K, H, BF16)
