@@ -1873,7 +1873,7 @@ cudaError_t bwd_type(const void* W, const void* bias, moe_dtype_t dtype, PairArg
             j.dw_part = a.dw_part;
             j.parts = parts;
             j.g = a.src;
-            j.bias = bias;
+            j.bias = d_weights ? bias : nullptr;  // part of d_weights only, and expert_idx with it
             j.expert_idx = expert_idx;
             j.d_weights = d_weights;
             j.T = T_;

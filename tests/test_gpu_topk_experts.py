@@ -391,3 +391,15 @@ def test_gradient_against_differences():
             moved[j].view(-1)[i] += 0.5
             num = (loss(*moved) - base) * 2
             assert abs(num - o[k].view(-1)[i].item()) <= 1e-9 * (1 + abs(num)), (k, i)
+
+
+@pytest.mark.parametrize("K", [1, 2, 5])
+@pytest.mark.parametrize("want", [("d_x",), ("dW",), ("db",), ("d_x", "dW", "db")], ids="+".join)
+def test_expert_indices_are_read_for_the_weights_gradient_only(want, K):
+    """Without d_weights the bias plays no part, and the routing may come without expert_idx."""
+    T, E, H = 300, 6, 128
+    x, W, b, g = _data(T, E, K, H, BF16)
+    routing, w = _routing(T, E, K)
+    bare = ops.Routing(None, routing.counts, routing.offsets, routing.perm)
+    o = _reference(x, W, b, g, routing.expert_idx, w)
+    _check_bwd(_bwd(x, W, b, g, bare, w, want), o, routing, K, H, want)
