@@ -164,11 +164,11 @@ __device__ __forceinline__ void softmax_stats(const float (&l)[VPL], int e0, int
     z = s == V(0) ? V(1) : s;
 }
 
-// Shared memory of one warp: per token of the warp K + 1 chosen experts and their keys'
+// Shared memory of one warp: per token of the warp its K chosen experts and their keys'
 // values, and with groups the values and the group scores.
 template <typename V>
 struct WarpSmem {
-    int* slot;    // [32 / LPT][K + 1]
+    int* slot;    // [32 / LPT][K]
     float* slot_v;
     V* val;       // [32 / LPT][E padded], group selection only
     V* gscore;    // [32 / LPT][G]
@@ -292,10 +292,9 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
             if (!((alive >> j) & 1u)) key[j] = 0;
     }
     constexpr bool kCheck = kFast && MODE != kLogits;
-    int* slot = sm.slot + tok * (R.K + 1);
-    float* slot_v = sm.slot_v + tok * (R.K + 1);
-    const int rounds = (kCheck && bias) ? R.K + 1 : R.K;
-    for (int k = 0; k < rounds; ++k) {
+    int* slot = sm.slot + tok * R.K;
+    float* slot_v = sm.slot_v + tok * R.K;
+    for (int k = 0; k < R.K; ++k) {
         Key best = 0;
         int at = 0;
 #pragma unroll
@@ -318,22 +317,34 @@ __device__ __forceinline__ bool choose(const float (&l)[VPL], const T* row, cons
         }
     }
     __syncwarp();
-    if (kCheck && bias) {
-        for (int k = sub; k < R.K; k += LPT) {
-            const int ea = slot[k], eb = slot[k + 1];
-            if (eb < 0) continue;
-            const float a = slot_v[k], b = slot_v[k + 1];
+    if constexpr (kCheck) {
+        if (bias) {
             // equal logits and equal biases are a true tie, in index order already
-            if (a - b <= tol * (1.0f + fabsf(a)) && !(to_f(row[ea]) == to_f(row[eb]) && bias[ea] == bias[eb])) unsure = true;
+            for (int k = sub; k + 1 < R.K; k += LPT) {
+                const int ea = slot[k], eb = slot[k + 1];
+                const float a = slot_v[k], b = slot_v[k + 1];
+                if (a - b <= tol * (1.0f + fabsf(a)) && !(to_f(row[ea]) == to_f(row[eb]) && bias[ea] == bias[eb])) unsure = true;
+            }
+            // Any expert left that comes near the last one chosen, not the next alone: that one may be a
+            // true tie with another, larger one behind it.
+            const float last = slot_v[R.K - 1], low = last - tol * (1.0f + fabsf(last));
+            if (last > -INFINITY) {
+                const int el = slot[R.K - 1];
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (key[j] > 1 && value_of(static_cast<uint32_t>(key[j])) >= low &&
+                        !(l[j] == to_f(row[el]) && bias[e0 + j] == bias[el]))
+                        unsure = true;
+            }
         }
     }
     return unsure;
 }
 
-// A whole warp on one token (fp32). A threshold that at least K (with the border test
-// K + 1) values reach gives a few candidates, a lane each, which are ranked by counting.
-// The threshold is the last token's, where that leaves between K + 1 and 32 candidates,
-// else the largest of the lanes' maxima that enough lanes reach. Returns false where the
+// A whole warp on one token (fp32). A threshold that at least K values reach gives a few
+// candidates, a lane each, which are ranked by counting. The threshold is the last token's,
+// where that leaves between K and 32 candidates, else the largest of the lanes' maxima that
+// enough lanes reach. Returns false where the
 // fp32 values leave the choice open, or more than 32 reach the threshold (equal values).
 // Dropped experts are NaN, which no comparison lets through; masked ones -inf.
 template <typename T, int VPL, int MODE>
@@ -411,7 +422,7 @@ __device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const
         for (int j = 0; j < VPL; ++j)
             if (order[j] == order[j]) order[j] = is_masked(l[j]) ? -INFINITY : l[j];
     }
-    const int need = check ? R.K + 1 : R.K;
+    const int need = R.K;
     int n = 0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) n += order[j] >= guess ? 1 : 0;
@@ -470,12 +481,27 @@ __device__ __forceinline__ bool choose_by_threshold(const float (&l)[VPL], const
     guess = guess == guess && fabsf(guess) < INFINITY ? guess + 0.25f * (at_guess - guess) : at_guess;
     if (check) {
         __syncwarp();
-        if (lane < R.K && lane + 1 < total) {
+        if (lane + 1 < R.K) {
             const float x = slot_v[lane], y = slot_v[lane + 1];
             if (x - y <= tol * (1.0f + fabsf(x))) {
                 // equal logits and equal biases are a true tie, in index order already
                 const int ea = slot[lane], eb = slot[lane + 1];
                 if (!(to_f(row[ea]) == to_f(row[eb]) && bias[ea] == bias[eb])) unsure = true;
+            }
+        }
+        // any expert left that comes near the last one chosen, as in choose()
+        const float last = slot_v[R.K - 1], low = last - tol * (1.0f + fabsf(last));
+        int near = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) near += order[j] >= low ? 1 : 0;
+        if (!keep) near = 0;
+        if (__reduce_add_sync(kFull, near) > R.K && last > -INFINITY) {
+            const int el = slot[R.K - 1];
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int e = e0 + j;
+                const bool left = keep && order[j] >= low && (order[j] < last || (order[j] == last && e > el));
+                if (left && !(to_f(row[e]) == to_f(row[el]) && bias[e] == bias[el])) unsure = true;
             }
         }
     }
@@ -535,7 +561,7 @@ __device__ __noinline__ void route_again(const T* row, int64_t t, bool vec, cons
     __syncwarp();
 }
 
-// Shared memory of one warp: slots of its tokens (K + 1 experts and values each), softmax
+// Shared memory of one warp: slots of its tokens (K experts and values each), softmax
 // statistics, candidates and their number, and with groups (8-byte elements, enough for
 // route_again) values and group scores.
 struct WarpArea {
@@ -551,7 +577,7 @@ struct WarpArea {
 __host__ __device__ inline int slot_tokens(int lpt, int K) { return lpt < 32 ? 32 / lpt : K <= 4 ? 8 : K <= 8 ? 4 : 2; }
 __host__ __device__ inline int warp_bytes(const Rule& R, int lpt, int vpl) {
     const int n = slot_tokens(lpt, R.K), tpw = 32 / lpt;
-    int b = n * (R.K + 1) * 8 + n * 8 + 256 + 8;
+    int b = n * R.K * 8 + n * 8 + 256 + 8;
     if (R.G > 1) {
         const int again = padded(lpt < 32 ? 64 : 32 * vpl) + R.G, now = (tpw * (padded(lpt * vpl) + R.G) + 1) / 2;
         b += 8 * (again > now ? again : now);
@@ -562,8 +588,8 @@ __device__ __forceinline__ WarpArea warp_area(uint8_t* p, int lpt, int K) {
     const int n = slot_tokens(lpt, K);
     WarpArea a;
     a.slot = reinterpret_cast<int*>(p);
-    a.slot_v = reinterpret_cast<float*>(p + n * (K + 1) * 4);
-    a.stats = reinterpret_cast<float2*>(p + n * (K + 1) * 8);
+    a.slot_v = reinterpret_cast<float*>(p + n * K * 4);
+    a.stats = reinterpret_cast<float2*>(p + n * K * 8);
     a.cand = reinterpret_cast<uint2*>(a.stats + n);
     a.found = reinterpret_cast<int*>(a.cand + 32);
     a.groups = reinterpret_cast<double*>(a.found + 2);
@@ -599,8 +625,8 @@ __device__ __forceinline__ void route_tokens(const T* logits, int64_t ld, int64_
                 const int64_t tn = t + step;
                 load_logits<T, VPL>(logits + (tn < t1 ? tn : 0) * ld, e0, R.E, vec, tn < t1, next);
                 float2 stats = make_float2(0.0f, 1.0f);
-                if (!choose_by_threshold<T, VPL, MODE>(l, b, logits + t * ld, bias, R, A.slot + i * (K + 1),
-                                                       A.slot_v + i * (K + 1), A.cand, A.found,
+                if (!choose_by_threshold<T, VPL, MODE>(l, b, logits + t * ld, bias, R, A.slot + i * K,
+                                                       A.slot_v + i * K, A.cand, A.found,
                                                        reinterpret_cast<float*>(A.groups), stats, guess))
                     open |= 1u << i;
                 if (lane == 0) A.stats[i] = stats;
@@ -610,7 +636,7 @@ __device__ __forceinline__ void route_tokens(const T* logits, int64_t ld, int64_
             const int i = lane / lanes, k = lane % lanes;
             const int64_t t = tb + i * step;
             const bool done = t < t1 && !((open >> i) & 1u), on = done && k < K;
-            const int e = on ? A.slot[i * (K + 1) + k] : 0;
+            const int e = on ? A.slot[i * K + k] : 0;
             const float x = on ? to_f(logits[t * ld + e]) : 0.0f;
             const float w = lanes == 4 ? weight_of<4>(x, on, A.stats[i], R)
                             : lanes == 8 ? weight_of<8>(x, on, A.stats[i], R) : weight_of<16>(x, on, A.stats[i], R);
@@ -641,7 +667,7 @@ __device__ __forceinline__ void route_tokens(const T* logits, int64_t ld, int64_
             float2 stats = make_float2(0.0f, 1.0f);
             if (!R.sigmoid && !R.renorm) softmax_stats<float, LPT, VPL>(l, e0, R.E, stats.x, stats.y);
             // K experts over LPT lanes, so the sums of a renormalised token take K / LPT turns
-            const int* slot = A.slot + tok * (K + 1);
+            const int* slot = A.slot + tok * K;
             float m = stats.x, z = stats.y;
             if (R.renorm) {
                 m = -INFINITY;

@@ -177,6 +177,36 @@ def test_values_that_fp32_cannot_tell_apart(E, score):
         _check(logits, R(E, 4, score, True, 1.0, G, TG, best), bias)
 
 
+@pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [5, 200, 3000])
+@pytest.mark.parametrize("E,K,groups", [(3, 1, 1), (3, 2, 1), (40, 6, 1), (64, 1, 1), (64, 6, 8), (65, 4, 1), (65, 1, 1), (256, 1, 1),
+                                        (256, 8, 1), (256, 8, 8)])
+def test_equal_values_at_the_border_beside_a_larger_one(E, K, groups, T, score):
+    """Exact ties across place K, and experts behind them that fp32 cannot tell from the tie: the largest
+    wins whatever its index. Sigmoid: bf16 steps near saturation under a bias of zero; softmax: logits a few
+    2^-24 E apart under a bias of 4, whose last place is 2^-21."""
+    g = torch.Generator(device="cuda").manual_seed(E + T)
+    if score == SIG:
+        logits = 10 + torch.randint(0, 96, (T, E), generator=g, device="cuda").float() / 16
+        logits[0] = 14.0
+        logits[0, E - 1] = 14.0625
+        bias = torch.zeros(E, device="cuda")
+    else:
+        logits = torch.randint(0, 4, (T, E), generator=g, device="cuda").float() * (E * 2.0 ** -24)
+        logits[0] = 0.0
+        logits[0, E - 1] = E * 2.0 ** -24
+        bias = torch.full((E,), 4.0, device="cuda")
+    # every other row has K + 3 of them, the rest far below
+    few = torch.rand(T, E, generator=g, device="cuda").argsort(1).argsort(1) < K + 3
+    logits[1::2] -= 16.0 * ~few[1::2]
+    logits = logits.to(BF16 if score == SIG else F32)
+    rule = R(E, K, score, True, 1.0, groups, max(1, groups // 2), 1 if groups == 1 else 2)
+    got, _ = _check(logits, rule, bias)
+    if groups == 1:
+        assert got["expert_idx"][0] == E - 1
+        got, _ = _check(logits, rule, torch.where(torch.arange(E, device="cuda") % 3 == 0, bias, bias + 0.25))
+
+
 @pytest.mark.parametrize("rule", [R(8, 3), R(8, 3, SOFT, True), R(40, 6, SIG, True), R(64, 6, SIG, True, 2.5, 8, 4, 2),
                                   R(256, 8, SOFT, True, 1.0, 8, 3, 1)], ids=_id)
 @pytest.mark.parametrize("with_bias", [False, True], ids=["plain", "bias"])
