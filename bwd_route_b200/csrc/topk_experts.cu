@@ -14,9 +14,8 @@
 //     ring, one warp streams the expert's weights by TMA (K-major for y, MN-major for
 //     d_x), one thread issues the MMAs into one of two tensor-memory accumulators, eight
 //     warps drain the other. With K = 1 a pair's row is the result; else it goes to the
-//     workspace as fp16 with a power of two per 32 columns (their largest value lands in
-//     [2^14, 2^15)): half of fp32's traffic at 11 bits, finer than bf16's 8, whatever the
-//     magnitude. The backward's epilogue also takes x . (W_e^T g) from the fp32
+//     workspace in fp32, so that a token's sum over k is fp32 from end to end and y and d_x
+//     are rounded once. The backward's epilogue also takes x . (W_e^T g) from the fp32
 //     accumulators, with its warps' rows of x brought in by cp.async beside them.
 //     Bound by shared memory: a chunk of 64 channels moves 96 KB (rows in, weights in, both
 //     read by the MMA) at 128 bytes a cycle, 768 cycles against the MMA's 512. 16,384
@@ -252,8 +251,7 @@ struct PairArgs {
     DivK by_k;
     int64_t P;
     void* out;             // [T][H]; d_x: may be NULL (only the weights' gradient)
-    __half* rows;          // [P][H], K > 1
-    float* scale;          // [P][H / 32], K > 1
+    float* rows;           // [P][H], K > 1
     float* dw_part;        // [parts][P], d_x with `other`
     DuoWs duo;             // K = 2: see duo_kernel
     uint32_t* flags;
@@ -489,11 +487,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
             for (int it = 0; it < 4; ++it) {
                 const int pr = __shfl_sync(kFull, p, it * 8 + R4);
                 there |= pr >= 0 ? 1u << it : 0u;
-                dst[it] = (ONE ? reinterpret_cast<uint8_t*>(out) : reinterpret_cast<uint8_t*>(A.rows)) +
-                          (static_cast<int64_t>(pr < 0 ? 0 : pr) * H + col0 + j4 * 8) * 2;
+                const int64_t at = static_cast<int64_t>(pr < 0 ? 0 : pr) * H + col0;
+                dst[it] = ONE ? reinterpret_cast<uint8_t*>(out + at + j4 * 8) : reinterpret_cast<uint8_t*>(A.rows + at + j4 * 4);
             }
             float dot = 0.0f;
-            float inv[HALF / 32];  // this lane's row: the powers its blocks were divided by
             uint32_t tm[2][32];
             if (ncols > 0) {
                 tmem_ld_32x32b_x32_async(tbase, tm[0]);
@@ -546,30 +543,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                         for (int j = 0; j < 8; ++j) v[8 * g + j] += to_f(bv.v[j]);
                     }
                 }
-                if (store) {
-                    float f = w;
-                    if (!ONE) {
-                        float m = 0.0f;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) m = fmaxf(m, fabsf(v[j]));
-                        if (m == INFINITY) {  // an infinite sum keeps its finite neighbours' bits
-                            m = 0.0f;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) m = fabsf(v[j]) < INFINITY ? fmaxf(m, fabsf(v[j])) : m;
-                        }
-                        // exponent of the largest |v w|, 40 at least: fp16's last step is then 2^-125
-                        const int ex = max(static_cast<int>((__float_as_uint(m * fabsf(w)) >> 23) & 255), 40);
-                        f = w * __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
-                        // only where |v w| is below 2^-87; an infinite or NaN weight stays what it is
-                        if (fabsf(w) < INFINITY) f = fminf(fmaxf(f, -3e38f), 3e38f);
-                        inv[i] = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
-                    }
+                if (store && ONE) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         float s[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) s[j] = v[8 * g + j] * f;
-                        st_shared_u4(stage + lane * 64 + ((g ^ swz) << 4), ONE ? pack8<T>(s) : pack8<__half>(s));
+                        for (int j = 0; j < 8; ++j) s[j] = v[8 * g + j] * w;
+                        st_shared_u4(stage + lane * 64 + ((g ^ swz) << 4), pack8<T>(s));
                     }
                     __syncwarp();
 #pragma unroll
@@ -578,19 +558,27 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_w, const PairArgs A) {
                         const uint4 val = ld_shared_u4(stage + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4));
                         if ((there >> it) & 1u) *reinterpret_cast<uint4*>(dst[it] + 2 * c) = val;
                     }
+                } else if (store) {
+                    // fp32: 16 columns at a time
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h) __syncwarp();
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int j = 16 * h + 4 * g;
+                            st_shared_v4(stage + lane * 64 + ((g ^ swz) << 4), v[j] * w, v[j + 1] * w, v[j + 2] * w, v[j + 3] * w);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int it = 0; it < 4; ++it) {
+                            const int R = it * 8 + R4;
+                            const float4 val = ld_shared_v4(stage + R * 64 + ((j4 ^ ((R >> 1) & 3)) << 4));
+                            if ((there >> it) & 1u) *reinterpret_cast<float4*>(dst[it] + 4 * (c + 16 * h)) = val;
+                        }
+                    }
                 }
                 __syncwarp();
                 if (more) tmem_ld_wait_tied(tm[(i + 1) & 1]);
-            }
-            if (!ONE && p >= 0 && ncols > 0 && (!DX || out)) {
-                float* sc = A.scale + static_cast<int64_t>(p) * (H / 32) + (col0 >> 5);
-                if (HALF == 128 && ncols == 128 && H % 128 == 0) {  // 16-byte aligned
-                    *reinterpret_cast<float4*>(sc) = make_float4(inv[0], inv[1 % (HALF / 32)], inv[2 % (HALF / 32)], inv[3 % (HALF / 32)]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < HALF / 32; ++i)
-                        if (32 * i < ncols) sc[i] = inv[i];
-                }
             }
             if (ncols <= 0) {
                 __syncwarp();
@@ -1093,8 +1081,7 @@ duo_kernel(const __grid_constant__ CUtensorMap tm_w, const DuoArgs A) {
 
 // ---------------------------------------------------------------- join
 struct JoinArgs {
-    const __half* rows;    // [P][H]
-    const float* scale;    // [P][H / 32]
+    const float* rows;     // [P][H]
     void* out;             // [T][H], or NULL
     const float* dw_part;  // [parts][P]; d_weights only
     int parts;
@@ -1107,7 +1094,7 @@ struct JoinArgs {
     int K, H;
 };
 
-// LPT lanes per token, 8 columns each at a time; U tokens per turn, so that enough loads
+// LPT lanes per token, four columns each at a time; U tokens per turn, so that enough loads
 // are on the way; KM: an upper bound of K. DW: the backward (d_weights may be NULL).
 template <typename T, int KM, int U, bool DW>
 __global__ void __launch_bounds__(256, KM <= 4 ? 4 : 2) join_kernel(const JoinArgs A, int LPT) {
@@ -1132,42 +1119,43 @@ __global__ void __launch_bounds__(256, KM <= 4 ? 4 : 2) join_kernel(const JoinAr
                 dot[u][k] = 0.0f;
             }
         }
-        for (int c = sub * 8; c < H; c += LPT * 8) {
-            Chunk<__half, 8> r[U][KM];
-            float f[U][KM];
-            Chunk<T, 8> gv[U];
+        for (int c = sub * 4; c < H; c += LPT * 4) {
+            Chunk<float, 4> r[U][KM];
+            Chunk<T, 4> gv[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (t[u] >= A.T) continue;
                 if (rows)
 #pragma unroll
                     for (int k = 0; k < KM; ++k)
-                        if (k < K) {
-                            r[u][k] = *reinterpret_cast<const Chunk<__half, 8>*>(A.rows + (t[u] * K + k) * H + c);
-                            f[u][k] = A.scale[(t[u] * K + k) * (H / 32) + (c >> 5)];
-                        }
-                if (DW && with_bias) gv[u] = *reinterpret_cast<const Chunk<T, 8>*>(static_cast<const T*>(A.g) + t[u] * H + c);
+                        if (k < K) r[u][k] = *reinterpret_cast<const Chunk<float, 4>*>(A.rows + (t[u] * K + k) * H + c);
+                if (DW && with_bias) gv[u] = *reinterpret_cast<const Chunk<T, 4>*>(static_cast<const T*>(A.g) + t[u] * H + c);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (t[u] >= A.T) continue;
-                float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                float s[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int k = 0; k < KM; ++k) {
                     if (k >= K) continue;
                     if (rows)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) s[i] = fmaf(to_f(r[u][k].v[i]), f[u][k], s[i]);
+                        for (int i = 0; i < 4; ++i) s[i] += r[u][k].v[i];
                     if (with_bias) {
-                        const Chunk<T, 8> bv = *reinterpret_cast<const Chunk<T, 8>*>(br[u][k] + c);
+                        const Chunk<T, 4> bv = *reinterpret_cast<const Chunk<T, 4>*>(br[u][k] + c);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 4; ++i) {
                             if (DW) dot[u][k] += to_f(gv[u].v[i]) * to_f(bv.v[i]);
                             else s[i] = fmaf(to_f(bv.v[i]), wk[u][k], s[i]);
                         }
                     }
                 }
-                if (rows) *reinterpret_cast<uint4*>(static_cast<T*>(A.out) + t[u] * H + c) = pack8<T>(s);
+                if (rows) {
+                    Chunk<T, 4> o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o.v[i] = from_f<T>(s[i]);
+                    *reinterpret_cast<Chunk<T, 4>*>(static_cast<T*>(A.out) + t[u] * H + c) = o;
+                }
             }
         }
         if (DW && A.d_weights) {
@@ -1752,12 +1740,12 @@ cudaError_t join_launch(const JoinArgs& a, int sms, cudaStream_t s) {
     // the most lanes a token that work seven eighths of the time (H 192, K 3, 224,532 tokens: 8 lanes
     // 76 us, 32 of which 24 work 112; H 832, K 3, 20,000 tokens: 8 lanes 41, 32 of which 26 work 36)
     int lpt = 32;
-    while (lpt > 8 && 8 * a.H < 7 * (lpt * 8) * ((a.H + lpt * 8 - 1) / (lpt * 8))) lpt /= 2;
+    while (lpt > 8 && 8 * a.H < 7 * (lpt * 4) * ((a.H + lpt * 4 - 1) / (lpt * 4))) lpt /= 2;
     auto go = [&](auto kernel, int u) {
         const int64_t tokens = 8 * (32 / lpt) * u, want = (a.T + tokens - 1) / tokens, cap = static_cast<int64_t>(sms) * 8;
         return launch_pdl(kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s, a, lpt);
     };
-    if (a.K <= 2) return DW ? go(join_kernel<T, 2, 1, DW>, 1) : go(join_kernel<T, 2, 2, DW>, 2);
+    if (a.K <= 2) return go(join_kernel<T, 2, DW ? 1 : 2, DW>, DW ? 1 : 2);
     if (a.K <= 4) return go(join_kernel<T, 4, 1, DW>, 1);
     if (a.K <= 8) return go(join_kernel<T, 8, 1, DW>, 1);
     return go(join_kernel<T, 16, 1, DW>, 1);
@@ -1819,7 +1807,6 @@ cudaError_t fwd_type(const void* W, moe_dtype_t dtype, const PairArgs& a, int64_
     if (e != cudaSuccess || a.K == 1) return e;
     JoinArgs j{};
     j.rows = a.rows;
-    j.scale = a.scale;
     j.out = a.out;
     j.bias = a.bias;
     j.expert_idx = expert_idx;
@@ -1868,7 +1855,6 @@ cudaError_t bwd_type(const void* W, const void* bias, moe_dtype_t dtype, PairArg
         if (e == cudaSuccess && (d_weights || (a.K > 1 && !duo))) {
             JoinArgs j{};
             j.rows = a.rows;
-            j.scale = a.scale;
             j.out = a.K > 1 && !duo ? a.out : nullptr;
             j.dw_part = a.dw_part;
             j.parts = parts;
@@ -1936,8 +1922,7 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
     a.H = H;
     a.P = static_cast<int64_t>(P);
     a.out = y;
-    a.rows = reinterpret_cast<__half*>(ws + L.rows);
-    a.scale = reinterpret_cast<float*>(ws + L.scale);
+    a.rows = reinterpret_cast<float*>(ws + L.rows);
     a.duo = {reinterpret_cast<int32_t*>(ws + L.duo), reinterpret_cast<int32_t*>(ws + L.list)};
     a.flags = reinterpret_cast<uint32_t*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1994,8 +1979,7 @@ moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dt
     a.H = H;
     a.P = static_cast<int64_t>(P);
     a.out = d_x;
-    a.rows = reinterpret_cast<__half*>(ws + L.rows);
-    a.scale = reinterpret_cast<float*>(ws + L.scale);
+    a.rows = reinterpret_cast<float*>(ws + L.rows);
     a.duo = {reinterpret_cast<int32_t*>(ws + L.duo), reinterpret_cast<int32_t*>(ws + L.list)};
     a.dw_part = reinterpret_cast<float*>(ws + L.dw_part);
     a.flags = reinterpret_cast<uint32_t*>(ws);

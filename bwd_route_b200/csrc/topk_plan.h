@@ -44,8 +44,7 @@ __host__ __device__ inline int wgrad_pieces(int n, int64_t P, int extra) {
 }
 
 struct ExpertsWs {
-    size_t rows = 0;     // fp16 [T * K][H]: the pairs' rows, K > 1
-    size_t scale = 0;    // float [T * K][H / 32]: their factors, K > 1
+    size_t rows = 0;     // float [T * K][H]: the pairs' rows, K > 1
     size_t dw_part = 0;  // float [ceil(H / 64) + 1][T * K]: column parts of the weights' gradient
     size_t duo = 0;      // int32 [3 * E * E + 1], K = 2: classes of tokens
     size_t list = 0;     // int32 [T], K = 2: tokens by class
@@ -65,8 +64,7 @@ inline ExpertsWs experts_ws(int64_t T, int E, int K, int H, size_t begin) {
         off = align_up(off + bytes, 256);
         return at;
     };
-    L.rows = take(K > 1 ? 2 * P * H : 0);
-    L.scale = take(K > 1 ? sizeof(float) * P * (H / 32) : 0);
+    L.rows = take(K > 1 ? sizeof(float) * P * H : 0);
     L.dw_part = take(sizeof(float) * nb * P);
     L.duo = take(K == 2 ? sizeof(int32_t) * (3 * static_cast<size_t>(E) * E + 1) : 0);
     L.list = take(K == 2 ? sizeof(int32_t) * T : 0);

@@ -117,10 +117,8 @@ moe_status_t moe_topk_route_bwd(const void* logits, moe_dtype_t dtype, int64_t T
  * x, y [T, H], W [E, H, H] (W[e][o][i], y = W x) and bias [E, H] (NULL: none) have
  * elements of `dtype`, MOE_DTYPE_BF16 or MOE_DTYPE_F16, and are dense and 16-byte
  * aligned; weights [T * K] float. routing is what moe_topk_route wrote (offsets,
- * perm and, with a bias, expert_idx are read). Products and sums over i are fp32 on the tensor cores; for K > 1
- * each of the K rows of a token waits for the others as fp16 with a power of two per
- * 32 columns (11 bits, no overflow), and the K are added in fp32 in the order of k;
- * the result is rounded once.
+ * perm and, with a bias, expert_idx are read). Products and sums over i are fp32 on the tensor cores, the K rows
+ * of a token are added in fp32, and the result is rounded once.
  * 1 <= E <= 256, 1 <= K <= min(16, E), H a multiple of 64 with 64 <= H <= 4096,
  * 0 <= T * K < 2^31 - 256. y overlaps no input. Needs the workspace.
  */

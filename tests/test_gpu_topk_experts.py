@@ -403,3 +403,32 @@ def test_expert_indices_are_read_for_the_weights_gradient_only(want, K):
     bare = ops.Routing(None, routing.counts, routing.offsets, routing.perm)
     o = _reference(x, W, b, g, routing.expert_idx, w)
     _check_bwd(_bwd(x, W, b, g, bare, w, want), o, routing, K, H, want)
+
+
+@pytest.mark.parametrize("T,E,K,H", [(5, 8, 2, 256), (129, 5, 3, 192), (300, 64, 8, 64), (40, 256, 16, 64), (700, 8, 2, 320),
+                                     (513, 7, 4, 512), (260, 6, 2, 1024), (5003, 4, 2, 128), (50000, 5, 2, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+def test_a_tokens_rows_are_added_in_fp32(T, E, K, H, dtype):
+    """y and d_x are rounded to 16 bits once, at the end: beside that rounding and the products' own bound
+    there are K roundings of fp32 and those of the bias, K u and 2 u of the magnitudes."""
+    x, W, b, g = _data(T, E, K, H, dtype)
+    routing, w = _routing(T, E, K)
+    o = _reference(x, W, b, g, routing.expert_idx, w)
+    got = {"y": _fwd(x, W, b, routing, w), "d_x": _bwd(x, W, b, g, routing, w, ("d_x",))["d_x"]}
+    f = torch.finfo(dtype)
+    for k, v in got.items():
+        fp32 = (2 * _acc(H) + (K + 2) * U) * o[k + "_acc"]
+        _within(k, v, o[k], fp32 + f.eps / 2 * (o[k].abs() + fp32) + f.smallest_normal * f.eps)
+
+
+@pytest.mark.parametrize("K", [1, 2, 4])
+def test_large_weights_of_tiny_rows(K):
+    """Rows of a few 2^-118 under weights of 2^119 and 2^120 are ordinary numbers."""
+    T, E, H = 200, 5, 128
+    x, W, _, g, w = _small_integers(T, E, K, H, 7)
+    routing, _ = _routing(T, E, K, 7)
+    X, WW, G = ((v * s).to(BF16).cuda() for v, s in ((x, 2.0 ** -60), (W, 2.0 ** -58), (g, 2.0 ** -60)))
+    ww = (w * 2.0 ** 120).cuda()
+    o = _reference(X, WW, None, G, routing.expert_idx, ww)
+    assert torch.equal(_fwd(X, WW, None, routing, ww).double(), o["y"])
+    assert torch.equal(_bwd(X, WW, None, G, routing, ww, ("d_x",))["d_x"].double(), o["d_x"])
