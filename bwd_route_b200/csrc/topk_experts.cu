@@ -30,7 +30,8 @@
 //   wgrad_kernel  : dW and db. The pairs are the contraction index: both operands are
 //     MN-major. Four warps gather rows of g and x by cp.async, eight scale the staged rows
 //     of g by w in place (rounded to the operand type: the weight depends on the pair, the
-//     contraction index, so it has to be in one operand) and add them up for db; a unit is a
+//     contraction index, so it has to be in one operand; fp16 with a power of two per expert
+//     from wgrad_peak_kernel) and add them up for db; a unit is a
 //     256 x 256 tile of dW[e] over a piece of e's pairs (topk_plan.h). 16,384 tokens, E 16,
 //     K 2, H 1024: 83 us, 0.83 PFLOP/s; a stage of 32 pairs moves 112 KB through shared
 //     memory (rows in, scaled, read by the MMAs), 875 cycles against the MMAs' 512. Stages
@@ -43,6 +44,7 @@
 // to 16 bits afterwards, shows it (relative error 1.0e-6 at H = 1024, 2e-7 at H = 128).
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "checks.h"
 #include "common.cuh"
@@ -1225,8 +1227,63 @@ struct WgradArgs {
     float* part;    // [slots][H][H]
     float* part_db; // [slots][H]
     int32_t* starts;  // [E + 1]: first slot of each expert, for wgrad_sum_kernel
+    uint32_t* peak;   // [E], fp16 with dW: see wgrad_peak_kernel
     uint32_t* flags;
 };
+
+// fp16: w g is staged times a power of two per expert that brings the expert's largest finite
+// |w g| to [2^14, 2^15), and the sums are divided by it. Unscaled, a term above 65,504 would
+// be infinite and one below 6e-5 would lose its bits, though dW itself is in range. `peak`: the
+// bits of that largest value; the factor's exponent is kept in range, for peaks above 2^-113.
+__device__ __forceinline__ int peak_exponent(uint32_t peak) { return max(static_cast<int>(peak >> 23), 15); }
+__device__ __forceinline__ float peak_factor(uint32_t peak) {
+    return __uint_as_float(static_cast<uint32_t>(268 - peak_exponent(peak)) << 23);
+}
+__device__ __forceinline__ float peak_inverse(uint32_t peak) {
+    return __uint_as_float(static_cast<uint32_t>(peak_exponent(peak) - 14) << 23);
+}
+
+// peak[e] (zeroed): bits of the largest finite |w g| over the pairs of expert e. A warp takes
+// eight slots of perm, a lane each, reads their rows of g and leaves one maximum per expert. Bound by L2: K reads
+// of g. fp16 only; 16,384 tokens, K 2, H 1024: 16 us.
+constexpr int kPeakSlots = 8;  // of a warp at a time: 32 of them leave most of the GPU idle (38 us)
+__global__ void __launch_bounds__(256) wgrad_peak_kernel(const WgradArgs A) {
+    griddep_wait();  // every global access below comes after the previous grid
+    __shared__ int off[kMaxE + 1];
+    for (int e = threadIdx.x; e <= A.E; e += 256) off[e] = A.offsets[e];
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * kPeakSlots;
+    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kPeakSlots; base < A.P; base += step) {
+        const bool valid = lane < kPeakSlots && base + lane < A.P;
+        const int pair = valid ? A.perm[base + lane] : 0;
+        const float w = valid ? fabsf(A.weights[pair]) : 0.0f;
+        const int e = valid ? span_of(off, A.E, static_cast<int>(base) + lane) : -1;
+        const int n = static_cast<int>(A.P - base < kPeakSlots ? A.P - base : kPeakSlots), token = A.by_k(pair);
+        uint32_t mine = 0;  // the largest finite |g| of this lane's row, as fp16
+        for (int i = 0; i < n; ++i) {
+            const int t = __shfl_sync(kFull, token, i);
+            const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __half*>(A.g) + static_cast<int64_t>(t) * A.H);
+            uint32_t m = 0;
+            for (int c = lane; c < A.H / 8; c += 32) {
+                const uint4 v = __ldg(row + c);
+                const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t a = word[j] & 0x7fff7fffu;
+                    m = __vmaxu2(m, a & __vcmpltu2(a, 0x7c007c00u));
+                }
+            }
+            m = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+            if (lane == i) mine = m;
+        }
+        float peak = w < INFINITY ? w * __half2float(__ushort_as_half(static_cast<unsigned short>(mine))) : 0.0f;
+        if (peak == INFINITY) peak = 3e38f;
+        const unsigned same = __match_any_sync(kFull, e);
+        const uint32_t most = __reduce_max_sync(same, __float_as_uint(peak));
+        if (e >= 0 && most != 0 && lane == __ffs(same) - 1) atomicMax(&A.peak[e], most);
+    }
+}
 
 // Pieces and slots of every expert, from the offsets in shared memory (warp 0).
 template <typename CtlT>
@@ -1245,6 +1302,7 @@ struct Unit {
 template <typename T>
 __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) {
     using C = WCfg;
+    constexpr bool kScaled = std::is_same<T, __half>::value;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* stg = smem + C::STAGES * C::STAGE;
@@ -1338,6 +1396,10 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
 #pragma unroll
                 for (int i = 0; i < N; ++i) w[i] = p[i] >= 0 ? A.weights[p[i]] : 0.0f;
             };
+            const float f = kScaled && A.peak ? peak_factor(A.peak[r.e]) : 1.0f;
+            auto scaled = [&](float w) {  // a finite weight stays finite (of a row of zeros, else f w is below 2^39)
+                return !kScaled ? w : fabsf(w) < INFINITY ? fminf(fmaxf(w * f, -3e38f), 3e38f) : w;
+            };
             pairs(r.lo, p0);
             pairs(r.lo + C::LOOK, p1);
             weights(p0, w0);
@@ -1350,7 +1412,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     ctl->row[slot][32 * i + lane] = p0[i] < 0 ? 0 : static_cast<int64_t>(A.by_k(p0[i])) * H;
-                    ctl->weight[slot][32 * i + lane] = w0[i];
+                    ctl->weight[slot][32 * i + lane] = scaled(w0[i]);
                     p0[i] = p1[i];
                     p1[i] = p2[i];
                     w0[i] = w1[i];
@@ -1472,6 +1534,7 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
             const int rows = min(kWTile, H - r.o0), cols = min(kWTile, H - r.i0);
             const bool on = lane * 8 < rows;
             const bool add = A.db && r.i0 == 0;
+            const float inv = kScaled && A.peak ? peak_inverse(A.peak[r.e]) : 1.0f;
             float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             for (int at = r.lo; ok && at < r.hi; at += C::LOOK) {
                 if (!(ok = mbar_wait(&ctl->lfull[slot], lphase, abort, A.flags))) break;
@@ -1534,6 +1597,9 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                     for (int k = 1; k < 8; ++k)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) db[j] += ctl->db[k][lane][j];
+                    if (kScaled)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) db[j] *= inv;
                     const int o = r.o0 + lane * 8;
                     if (r.pieces == 1) {
                         *reinterpret_cast<uint4*>(static_cast<T*>(A.db) + static_cast<int64_t>(r.e) * H + o) = pack8<T>(db);
@@ -1553,6 +1619,9 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                 for (int c = ch * 128; c < min(cols, ch * 128 + 128); c += 32) {
                     float v[32];
                     tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(mh * 256 + c), v);
+                    if (kScaled)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] *= inv;
                     if (r.pieces == 1) {
                         // 32 rows x 64 bytes through shared memory: 4 lanes a row, 8 rows an instruction
 #pragma unroll
@@ -1818,10 +1887,19 @@ cudaError_t fwd_type(const void* W, moe_dtype_t dtype, const PairArgs& a, int64_
 }
 
 template <typename T>
-cudaError_t wgrad_launch(const WgradArgs& a, int sms, cudaStream_t s) {
+cudaError_t wgrad_launch(WgradArgs a, int sms, cudaStream_t s) {
     static std::atomic<uint64_t> ready;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(wgrad_kernel<T>), kWSmem, ready);
     if (e != cudaSuccess) return e;
+    if (std::is_same<T, __half>::value && a.dW) {
+        e = cudaMemsetAsync(a.peak, 0, sizeof(uint32_t) * a.E, s);
+        if (e != cudaSuccess) return e;
+        const int64_t want = (a.P + 8 * kPeakSlots - 1) / (8 * kPeakSlots), cap = static_cast<int64_t>(sms) * 8;
+        e = launch_pdl(wgrad_peak_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s, a);
+        if (e != cudaSuccess) return e;
+    } else {
+        a.peak = nullptr;
+    }
     const int64_t hit = a.P < a.E ? a.P : a.E;
     const int64_t units = (hit + a.extra) * wgrad_tiles(a.H);
     e = launch_pdl(wgrad_kernel<T>, dim3(static_cast<unsigned>(units < sms ? units : sms)), dim3(kWThreads), kWSmem, s, a);
@@ -2000,6 +2078,7 @@ moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dt
     g.part = reinterpret_cast<float*>(ws + L.part);
     g.part_db = reinterpret_cast<float*>(ws + L.part_db);
     g.starts = reinterpret_cast<int32_t*>(ws + L.starts);
+    g.peak = reinterpret_cast<uint32_t*>(ws + L.peak);
     g.flags = a.flags;
     return cuda_status(dtype == MOE_DTYPE_BF16
                            ? bwd_type<__nv_bfloat16>(W, bias, dtype, a, g, T, routing->expert_idx, d_weights, sms, s)

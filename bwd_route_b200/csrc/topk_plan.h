@@ -51,6 +51,7 @@ struct ExpertsWs {
     size_t part = 0;     // float [2 * extra][H][H]
     size_t part_db = 0;  // float [2 * extra][H]
     size_t starts = 0;   // int32 [E + 1]: first slot of each expert
+    size_t peak = 0;     // uint32 [E]: bits of each expert's largest |w g|, fp16
     size_t total = 0;
 };
 
@@ -71,6 +72,7 @@ inline ExpertsWs experts_ws(int64_t T, int E, int K, int H, size_t begin) {
     L.part = take(sizeof(float) * slots * H * H);
     L.part_db = take(sizeof(float) * slots * H);
     L.starts = take(sizeof(int32_t) * (static_cast<size_t>(E) + 1));
+    L.peak = take(sizeof(uint32_t) * static_cast<size_t>(E));
     L.total = off;
     return L;
 }

@@ -432,3 +432,49 @@ def test_large_weights_of_tiny_rows(K):
     o = _reference(X, WW, None, G, routing.expert_idx, ww)
     assert torch.equal(_fwd(X, WW, None, routing, ww).double(), o["y"])
     assert torch.equal(_bwd(X, WW, None, G, routing, ww, ("d_x",))["d_x"].double(), o["d_x"])
+
+
+@pytest.mark.parametrize("T,E,K,H", [(300, 4, 2, 128), (5003, 4, 2, 128), (700, 8, 3, 320), (3000, 2, 1, 512), (50000, 6, 2, 64)])
+@pytest.mark.parametrize("w_to,g_rms,x_rms", [(16.0, 6000.0, 1e-3), (1000.0, 6000.0, 1e-5), (0.1, 1e-5, 1.0), (0.1, 1e-6, 30.0),
+                                              (1e-6, 1.0, 3e3)])
+def test_fp16_weight_gradient_whatever_the_terms_size(T, E, K, H, w_to, g_rms, x_rms):
+    """w d_out leaves fp16's range above or below, dW itself does not. Beside the bounds at the top a term
+    is off by 2^-39 of its expert's largest at most (half of fp16's last step, the largest brought to
+    2^14), and the result by half of the type's last step."""
+    x, W, b, g = _data(T, E, K, H, F16)
+    x, g = (x.float() * x_rms).to(F16), (g.float() * g_rms).to(F16)
+    assert torch.isfinite(g).all() and torch.isfinite(x).all()
+    routing, _ = _routing(T, E, K)
+    w = torch.rand(T, K, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") * w_to
+    o = _reference(x, W, b, g, routing.expert_idx, w)
+    got = _bwd(x, W, b, g, routing, w, ("dW", "db"))
+    assert o["dW"].abs().max() < 6e4
+    f = torch.finfo(F16)
+    r, n = f.eps / 2, int(routing.counts.max())
+    last = n * 2.0 ** -39 * (w.max() * g.abs().max().float() * x.abs().max().float()).double()
+    fp32 = 8 * r * o["dW_sq"].sqrt() + _acc(n) * 2 * o["dW_abs"] + last
+    _within("dW", got["dW"], o["dW"], fp32 + r * (o["dW"].abs() + fp32) + f.smallest_normal * r)
+    fp32 = (n + 2) * U * o["db_abs"]
+    in_range = o["db"].abs() < 6e4
+    _within("db", got["db"][in_range], o["db"][in_range], (fp32 + r * (o["db"].abs() + fp32) + f.smallest_normal * r)[in_range])
+
+
+def test_fp16_weight_gradient_of_rows_of_zeros_and_infinities():
+    """A huge weight over a row of zeros adds nothing; an infinite d_out reaches its own experts only."""
+    T, E, K, H = 300, 6, 2, 128
+    x, W, b, g = _data(T, E, K, H, F16)
+    routing, w = _routing(T, E, K)
+    g[5] = 0
+    want = _bwd(x, W, b, g, routing, w, ("dW", "db"))
+    huge = w.clone()
+    huge[5] = 3e38
+    got = _bwd(x, W, b, g, routing, huge, ("dW", "db"))
+    assert torch.equal(got["dW"], want["dW"]) and torch.equal(got["db"], want["db"])
+    bad = g.clone()
+    bad[7, 3] = float("inf")
+    hit = torch.zeros(E, dtype=torch.bool, device="cuda")
+    hit[routing.expert_idx.view(T, K)[7].long()] = True
+    got = _bwd(x, W, b, bad, routing, w, ("dW", "db"))
+    assert torch.equal(got["dW"][~hit], want["dW"][~hit]) and torch.equal(got["db"][~hit], want["db"][~hit])
+    rows = torch.arange(H, device="cuda") != 3
+    assert torch.isfinite(got["dW"][hit][:, rows]).all() and not torch.isfinite(got["dW"][hit][:, 3]).any()
