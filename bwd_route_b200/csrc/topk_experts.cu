@@ -28,14 +28,16 @@
 //     rounding; in the backward also d_w from the column parts and g . b_e. 16,384 tokens,
 //     K 2, H 1024: 30 us for 138 MB (4.6 TB/s, in part from L2).
 //   wgrad_kernel  : dW and db. The pairs are the contraction index: both operands are
-//     MN-major. Four warps gather rows of g and x by cp.async, eight scale the staged rows
-//     of g by w in place (rounded to the operand type: the weight depends on the pair, the
-//     contraction index, so it has to be in one operand; fp16 with a power of two per expert
-//     from wgrad_peak_kernel) and add them up for db; a unit is a
+//     MN-major. Four warps gather rows of g and x by cp.async, eight multiply the staged rows
+//     of g by w (the weight depends on the pair, the contraction index, so it has to be in one
+//     operand), leave the products as two 16-bit numbers each for the MMAs (fp16 with a power of
+//     two per expert from wgrad_peak_kernel) and add them up for db; a unit is a
 //     256 x 256 tile of dW[e] over a piece of e's pairs (topk_plan.h). 16,384 tokens, E 16,
-//     K 2, H 1024: 83 us, 0.83 PFLOP/s; a stage of 32 pairs moves 112 KB through shared
-//     memory (rows in, scaled, read by the MMAs), 875 cycles against the MMAs' 512. Stages
-//     of 64 pairs were no faster.
+//     K 2, H 1024: 123 us, 0.56 PFLOP/s of dW alone; a stage of 32 pairs moves 176 KB through
+//     shared memory (rows in, two parts out, read by the MMAs), 1375 cycles. One part, rounded,
+//     takes 85 us at that size and leaves dW's relative error at 2.3e-3 in bf16 where the rounding
+//     of the result alone gives 1.7e-3, as two parts do. A third group of four scaling warps was
+//     slower (141 us for the call instead of 130), as their registers then are fewer.
 //   wgrad_sum_kernel: adds the pieces of cut experts in order; zeros for experts without
 //     pairs. 6 us at that size.
 //
@@ -1188,8 +1190,8 @@ struct WCfg {
     static constexpr int RW = KT / 4;          // rows of a stage a warp gathers, or scales
     static constexpr int GROUP = KT * 128;     // 64 columns of a stage's rows
     static constexpr int OP = 4 * GROUP;       // 256 columns
-    static constexpr int STAGE = 2 * OP;       // g then x: 32 KiB
-    static constexpr int STAGES = 6;
+    static constexpr int STAGE = 3 * OP;       // w g's upper part (before: g), x, w g's lower part: 48 KiB
+    static constexpr int STAGES = 4;
     static constexpr int STG = 8 * 32 * 64;    // staging: 32 rows x 64 bytes a warp
     static constexpr int LOOK = 128;           // pairs looked up at a time
     static constexpr int LOOKS = 3;            // blocks of them on the way
@@ -1298,6 +1300,29 @@ __device__ __forceinline__ void piece_starts(CtlT* ctl, int E, int64_t P, int ex
 struct Unit {
     int e, piece, pieces, lo, hi, o0, i0;
 };
+
+// Two 16-bit numbers that add up to s: the upper one is s cut off, always of a smaller
+// magnitude, the lower one the rest, rounded (16 bits of s for bf16, 22 for fp16). So both have
+// the sign of s, and an infinite x times either is the same infinity; an infinite s is infinite
+// in both. Masks rather than conversions back and forth: 124 us instead of 141 at the size above.
+template <typename T>
+__device__ __forceinline__ void split8(const float (&s)[8], uint4& hi, uint4& lo) {
+    constexpr uint32_t kKeep = std::is_same<T, __half>::value ? 0xffffe000u : 0xffff0000u;
+    float h[8], l[8], most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        h[i] = __uint_as_float(__float_as_uint(s[i] * (1.0f - 0x1p-24f)) & kKeep);
+        l[i] = s[i] - h[i];
+        most = fmaxf(most, fabsf(s[i]));
+    }
+    if (most == INFINITY) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(s[i]) == INFINITY) l[i] = s[i];
+    }
+    hi = pack8<T>(h);
+    lo = pack8<T>(l);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) {
@@ -1497,9 +1522,13 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
 #pragma unroll
                     for (int ks = 0; ks < C::KT / 16; ++ks) {
                         const uint32_t on = ks != 0 ? 1u : p0 != r.lo;
-                        mma_f16(leader, tmem, gl + ks * kMnStep, kDescHi, xl + ks * kMnStep, kDescHi, idesc, on);
-                        if (halves == 2)
-                            mma_f16(leader, tmem + 256, gl + (2 * C::GROUP >> 4) + ks * kMnStep, kDescHi, xl + ks * kMnStep, kDescHi, idesc, on);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (h >= halves) break;
+                            const uint32_t a = gl + (2 * h * C::GROUP >> 4) + ks * kMnStep;
+                            mma_f16(leader, tmem + 256 * h, a, kDescHi, xl + ks * kMnStep, kDescHi, idesc, on);
+                            mma_f16(leader, tmem + 256 * h, a + (2 * C::OP >> 4), kDescHi, xl + ks * kMnStep, kDescHi, idesc, 1u);
+                        }
                     }
                     commit_f16(leader, &ctl->empty[stage]);
                     if (++stage == C::STAGES) {
@@ -1567,7 +1596,10 @@ __global__ void __launch_bounds__(kWThreads, 1) wgrad_kernel(const WgradArgs A) 
                                     if (add)
 #pragma unroll
                                         for (int j = 0; j < 8; ++j) db[j] += s[j];
-                                    st_shared_u4(to[i] + base, pack8<T>(s));
+                                    uint4 upper, lower;
+                                    split8<T>(s, upper, lower);
+                                    st_shared_u4(to[i] + base, upper);
+                                    st_shared_u4(to[i] + base + 2 * C::OP, lower);
                                 }
                             }
                         }

@@ -135,9 +135,10 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
  *   d_weights[t, k] = sum_o d_out[t, o] (sum_i W[e, o, i] x[t, i] + bias[e, o])
  * d_x, dW and db have elements of `dtype`, d_weights [T * K] is float. Any of them may
  * be NULL to skip it; an expert without pairs gets zeros in dW and db. d_weights comes
- * from fp32 sums throughout; d_x rounds as y does above; for dW the rows w d_out are
- * rounded to `dtype` for the tensor cores (fp32 sums, one rounding at the end), for db
- * they are not. Sums over tokens have a fixed order. bias is read for d_weights only.
+ * from fp32 sums throughout; d_x rounds as y does above; for dW every w d_out enters the
+ * tensor cores as two numbers of `dtype` that add up to it (its upper 16 bits for bf16, 22
+ * for fp16, whatever its size; fp32 sums, one rounding at the end), for db it is fp32.
+ * Sums over tokens have a fixed order. bias is read for d_weights only.
  * Outputs overlap neither each other nor an input. Needs the workspace.
  */
 moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dtype_t dtype,

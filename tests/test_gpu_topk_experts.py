@@ -478,3 +478,48 @@ def test_fp16_weight_gradient_of_rows_of_zeros_and_infinities():
     assert torch.equal(got["dW"][~hit], want["dW"][~hit]) and torch.equal(got["db"][~hit], want["db"][~hit])
     rows = torch.arange(H, device="cuda") != 3
     assert torch.isfinite(got["dW"][hit][:, rows]).all() and not torch.isfinite(got["dW"][hit][:, 3]).any()
+
+
+def _check_dW(got, o, routing):
+    """The rows w g are two 16-bit numbers each: the upper one leaves at most one of its steps, the lower
+    one rounds that to half of its own, so a term is off by eps r of itself at most (2^-15 bf16, 2^-21
+    fp16), independently of the others (Hoeffding, as above); their products are 2 n terms of a sum."""
+    f = torch.finfo(got.dtype)
+    r, n = f.eps / 2, int(routing.counts.max())
+    fp32 = 8 * f.eps * r * o["dW_sq"].sqrt() + _acc(2 * n) * 2 * o["dW_abs"]
+    _within("dW", got, o["dW"], fp32 + r * (o["dW"].abs() + fp32) + f.smallest_normal * r)
+
+
+@pytest.mark.parametrize("T,E,K,H", [(1, 4, 2, 128), (5, 8, 1, 256), (129, 5, 3, 192), (300, 64, 8, 64), (700, 8, 2, 320),
+                                     (513, 7, 4, 512), (260, 6, 2, 1024), (5003, 4, 2, 128), (9001, 13, 1, 640)])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+def test_weight_gradient_is_that_of_fp32_terms(T, E, K, H, dtype):
+    x, W, b, g = _data(T, E, K, H, dtype)
+    routing, w = _routing(T, E, K)
+    for v in (w, torch.ones_like(w), -w.round(decimals=1)):
+        o = _reference(x, W, b, g, routing.expert_idx, v)
+        _check_dW(_bwd(x, W, b, g, routing, v, ("dW",))["dW"], o, routing)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=str)
+@pytest.mark.parametrize("one", [False, True], ids=["weights", "ones"])
+def test_infinities_in_the_weight_gradient_are_those_of_the_formula(one, dtype):
+    """An infinite x or d_out makes its column or row of dW infinite, with the sign of the other factor,
+    and leaves everything else as it was."""
+    T, E, K, H = 300, 5, 2, 128
+    x, W, b, g = _data(T, E, K, H, dtype)
+    routing, w = _routing(T, E, K)
+    w = torch.ones_like(w) if one else w
+    hit = torch.zeros(E, dtype=torch.bool, device="cuda")
+    hit[routing.expert_idx.view(T, K)[7].long()] = True
+    assert (g[7] != 0).all() and (x[7] != 0).all() and hit.any() and not hit.all()
+    want = _bwd(x, W, b, g, routing, w, ("dW",))["dW"]
+    for name in ("x", "g"):
+        bx, bg = x.clone(), g.clone()
+        (bx if name == "x" else bg)[7, 3] = float("inf")
+        got = _bwd(bx, W, b, bg, routing, w, ("dW",))["dW"]
+        line = got[:, :, 3] if name == "x" else got[:, 3, :]
+        signs = torch.sign((g if name == "x" else x)[7].float())
+        assert torch.equal(line[hit].float(), (signs * float("inf")).expand(int(hit.sum()), H))
+        line[hit] = (want[:, :, 3] if name == "x" else want[:, 3, :])[hit]
+        assert torch.equal(got, want)
