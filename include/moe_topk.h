@@ -16,8 +16,10 @@
  * Errors.  Arguments are checked on the host before anything is launched; a bad
  *   argument returns a status and enqueues nothing. Device values are trusted:
  *   a routing must be what moe_topk_route wrote for the same tokens.
- * Determinism.  For the same inputs and device every output is the same from run
- *   to run, bit for bit: fixed-order sums, no floating-point atomics.
+ * Determinism.  For the same inputs, sizes, alignments and device every output is the
+ *   same from run to run, bit for bit: fixed-order sums, no floating-point atomics. The
+ *   order itself goes by sizes and alignments, so a token's last bits may differ between
+ *   calls of different T, or with arrays that start elsewhere.
  */
 #ifndef MOE_TOPK_H
 #define MOE_TOPK_H
@@ -116,9 +118,13 @@ moe_status_t moe_topk_route_bwd(const void* logits, moe_dtype_t dtype, int64_t T
  *   y[t, o] = sum_k w (sum_i W[e, o, i] x[t, i] + bias[e, o])
  * x, y [T, H], W [E, H, H] (W[e][o][i], y = W x) and bias [E, H] (NULL: none) have
  * elements of `dtype`, MOE_DTYPE_BF16 or MOE_DTYPE_F16, and are dense and 16-byte
- * aligned; weights [T * K] float. routing is what moe_topk_route wrote (offsets,
- * perm and, with a bias, expert_idx are read). Products and sums over i are fp32 on the tensor cores, the K rows
- * of a token are added in fp32, and the result is rounded once.
+ * aligned; weights [T * K] float. routing is what moe_topk_route wrote, all of it from one
+ * call: for K = 2 and many tokens expert_idx is read in place of offsets and perm wherever
+ * it is given, bias or not (tokens are then grouped by their two experts), else offsets and
+ * perm are, and with a bias and K > 1 expert_idx too. It may be NULL where there is no bias
+ * or K = 1. Products and sums over i are fp32 on the tensor cores, the K rows of a token are
+ * added in fp32, in the order of k (grouped: the lower expert first), and the result is
+ * rounded once.
  * 1 <= E <= 256, 1 <= K <= min(16, E), H a multiple of 64 with 64 <= H <= 4096,
  * 0 <= T * K < 2^31 - 256. y overlaps no input. Needs the workspace.
  */
@@ -138,7 +144,8 @@ moe_status_t moe_topk_fwd(const void* x, const void* W, const void* bias, moe_dt
  * from fp32 sums throughout; d_x rounds as y does above; for dW every w d_out enters the
  * tensor cores as two numbers of `dtype` that add up to it (its upper 16 bits for bf16, 22
  * for fp16, whatever its size; fp32 sums, one rounding at the end), for db it is fp32.
- * Sums over tokens have a fixed order. bias is read for d_weights only.
+ * Sums over tokens have a fixed order. bias is read for d_weights only; routing as above,
+ * and expert_idx may be NULL unless d_weights and a bias are given.
  * Outputs overlap neither each other nor an input. Needs the workspace.
  */
 moe_status_t moe_topk_bwd(const void* x, const void* W, const void* bias, moe_dtype_t dtype,

@@ -523,3 +523,15 @@ def test_infinities_in_the_weight_gradient_are_those_of_the_formula(one, dtype):
         assert torch.equal(line[hit].float(), (signs * float("inf")).expand(int(hit.sum()), H))
         line[hit] = (want[:, :, 3] if name == "x" else want[:, 3, :])[hit]
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T", [40000, 50000])
+def test_two_experts_without_expert_indices(T):
+    """Without a bias expert_idx may be left out: the tokens are then not grouped by it."""
+    E, K, H = 5, 2, 128
+    x, W, _, g = _data(T, E, K, H, BF16)
+    routing, w = _routing(T, E, K)
+    bare = ops.Routing(None, routing.counts, routing.offsets, routing.perm)
+    o = _reference(x, W, None, g, routing.expert_idx, w)
+    _check_rows("y", _fwd(x, W, None, bare, w), o, K, H)
+    _check_bwd(_bwd(x, W, None, g, bare, w), o, bare, K, H)
