@@ -15,9 +15,9 @@
 // row for every four threads: 17 us (a warp for a row: 111).
 //
 // dgamma and dbeta: a thread always sees the same columns, so it adds up its rows in
-// registers; every kFlush rows it adds that to its shared-memory sums (two levels, so
-// that no fp32 chain grows with T), the block's row teams are added in order, and a
-// second kernel adds the blocks in order. No atomics: the same bits from run to run.
+// registers; every kFlush rows it adds that to its shared-memory sums (so an fp32 chain grows
+// by one addition per 64 rows of a team, a few hundred for as many rows as memory holds), the
+// block's row teams are added in order, and a second kernel adds the blocks in order. No atomics: the same bits from run to run.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -185,7 +185,7 @@ __device__ __forceinline__ int span_of(const int* start, int n, int v) {
     return lo;
 }
 
-// start[i] = exclusive sum of count(0 .. i), start[n] = total; one warp, n <= 32 * 8.
+// start[i] = exclusive sum of count(0 .. i), start[n] = total; one warp, any n.
 template <typename F>
 __device__ __forceinline__ void warp_starts(int* start, int n, F count) {
     const int lane = threadIdx.x & 31;
