@@ -72,8 +72,9 @@ size_t moe_topk_workspace_bytes(int64_t T, int32_t E, int32_t K, int32_t H);
  * Router. For every token t, from logits[t, 0..E) (elements of `dtype`, rows ld >= E
  * elements apart):
  *   s[e] = softmax or logistic function of the logits,   v[e] = s[e] + bias[e]
- *   an expert whose logit is -inf or NaN (or whose v is NaN, as every softmax score
- *     of a row with a NaN or +inf is) is masked: v[e] = -inf, behind all others
+ *   an expert whose logit is -inf or NaN is masked: v[e] = -inf, behind all others; so is
+ *     one whose v is NaN where v is what is compared (with a bias, or sums of a group's two
+ *     best), as every softmax score of a row with a NaN or +inf is
  *   with groups: a group's score is the sum of its group_best largest v; the
  *     top_groups groups with the largest scores stay (ties: the lower group)
  *   the K experts with the largest v among those that stay are chosen, largest

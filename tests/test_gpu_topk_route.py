@@ -242,6 +242,21 @@ def test_nan_is_never_chosen_over_a_number():
     assert np.isfinite(got["weights"][[0, 1, 3, 4]]).all() and np.isnan(got["weights"][2]).all()
 
 
+@pytest.mark.parametrize("with_bias", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [8, 40, 100, 256])
+@pytest.mark.parametrize("T", [5, 400])
+def test_rows_with_a_nan_or_an_infinity(T, E, score, renorm, with_bias):
+    """Without a bias the logits alone are compared; with one, a softmax row with a NaN or +inf has only
+    NaN to compare, and its experts come by index."""
+    logits, bias = _logits(T, E, F32, 9)
+    logits[0, 3], logits[1, 5], logits[3, E - 1] = float("nan"), float("inf"), float("inf")
+    got, _ = _check(logits, R(E, 4, score, renorm), bias if with_bias else None)
+    if with_bias and score == SOFT:
+        assert (got["expert_idx"].reshape(T, 4)[[0, 1, 3]] == np.arange(4)).all()
+
+
 @pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
 @pytest.mark.parametrize("E", [8, 40, 100, 256])
 @pytest.mark.parametrize("T", [5, 3000])
