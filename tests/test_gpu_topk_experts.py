@@ -535,3 +535,26 @@ def test_two_experts_without_expert_indices(T):
     o = _reference(x, W, None, g, routing.expert_idx, w)
     _check_rows("y", _fwd(x, W, None, bare, w), o, K, H)
     _check_bwd(_bwd(x, W, None, g, bare, w), o, bare, K, H)
+
+
+@pytest.mark.parametrize("T,E,K,H,dtype", [(40, 3, 2, 4096, BF16), (300, 2, 1, 4096, F16), (130, 2, 2, 2048, F16),
+                                           (100000, 8, 1, 256, BF16), (60000, 8, 2, 256, F16), (20001, 12, 8, 128, BF16),
+                                           (9000, 20, 16, 64, F16)])
+def test_the_ends_of_the_range(T, E, K, H, dtype):
+    """The widest rows, one expert for many tokens, many experts a token, fp16 in the grouped path."""
+    x, W, b, g = _data(T, E, K, H, dtype)
+    routing, w = _routing(T, E, K, 5, 0.5)
+    o = _reference(x, W, b, g, routing.expert_idx, w)
+    _check_rows("y", _fwd(x, W, b, routing, w), o, K, H)
+    got = _bwd(x, W, b, g, routing, w)
+    _check_bwd(got, o, routing, K, H)
+    _check_dW(got["dW"], o, routing)
+
+
+@pytest.mark.parametrize("want", [("d_x",), ("d_weights",), ("dW",), ("db",), ("db", "d_weights")], ids="+".join)
+def test_some_outputs_of_grouped_tokens(want):
+    T, E, K, H = 50000, 5, 2, 192
+    x, W, b, g = _data(T, E, K, H, BF16)
+    routing, w = _routing(T, E, K)
+    o = _reference(x, W, b, g, routing.expert_idx, w)
+    _check_bwd(_bwd(x, W, b, g, routing, w, want), o, routing, K, H, want)

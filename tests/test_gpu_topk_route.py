@@ -149,6 +149,17 @@ def test_route_many_tokens(E, K, T):
     _check(logits, R(E, K, SOFT, True))
 
 
+@pytest.mark.parametrize("E,K,groups,top", [(256, 8, 8, 2), (256, 8, 4, 1), (192, 8, 6, 2), (256, 16, 8, 2), (256, 16, 2, 1), (128, 8, 8, 1)])
+@pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
+def test_few_groups_that_stay(E, K, groups, top, score):
+    """As few lanes hold the experts that stay as a token chooses experts, or fewer."""
+    for T, dtype in ((100, F32), (3000, BF16)):
+        logits, bias = _logits(T, E, dtype, E + K)
+        for best in (1, 2):
+            _check(logits, R(E, K, score, True, 1.0, groups, top, best), bias)
+            _check(logits, R(E, K, score, False, 1.0, groups, top, best))
+
+
 @pytest.mark.parametrize("rule", [r for r in RULES if r.E >= 4], ids=_id)
 def test_equal_values_go_to_the_lowest_index(rule):
     g = torch.Generator(device="cuda").manual_seed(1)
