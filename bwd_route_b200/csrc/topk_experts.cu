@@ -18,15 +18,17 @@
 //     are rounded once. The backward's epilogue also takes x . (W_e^T g) from the fp32
 //     accumulators, with its warps' rows of x brought in by cp.async beside them.
 //     Bound by shared memory: a chunk of 64 channels moves 96 KB (rows in, weights in, both
-//     read by the MMA) at 128 bytes a cycle, 768 cycles against the MMA's 512. 16,384
-//     tokens, E 16, K 2, H 1024, d_x: 69 us, 1.0 PFLOP/s (62 % of a library product's).
+//     read by the MMA) at 128 bytes a cycle, 768 cycles against the MMA's 512, and an epilogue
+//     that moves 8 bytes a value through it. 16,384 tokens, E 16, K 2, H 1024, d_x: 78 us,
+//     0.88 PFLOP/s (54 % of a library product's); 16-bit rows with a power of two per 32
+//     columns took 69, but carried a rounding of 11 bits for each of the K.
 //   duo_kernel    : y and d_x for K = 2 and many tokens: see there. 262,144 tokens, E 8,
 //     H 256, y: 81 us and 13 for the grouping, 0.85 PFLOP/s and 3.3 TB/s (floor 42 us by
 //     either); bound by the epilogue's chain (tensor memory, two weights, rounding,
 //     transpose, store), the tensor pipe runs 40 % of the time.
 //   join_kernel   : adds the K rows of a token (and w b_e) in the order of k in fp32, one
 //     rounding; in the backward also d_w from the column parts and g . b_e. 16,384 tokens,
-//     K 2, H 1024: 30 us for 138 MB (4.6 TB/s, in part from L2).
+//     K 2, H 1024, backward: 47 us for 201 MB (4.3 TB/s, in part from L2).
 //   wgrad_kernel  : dW and db. The pairs are the contraction index: both operands are
 //     MN-major. Four warps gather rows of g and x by cp.async, eight multiply the staged rows
 //     of g by w (the weight depends on the pair, the contraction index, so it has to be in one
@@ -39,7 +41,7 @@
 //     of the result alone gives 1.7e-3, as two parts do. A third group of four scaling warps was
 //     slower (141 us for the call instead of 130), as their registers then are fewer.
 //   wgrad_sum_kernel: adds the pieces of cut experts in order; zeros for experts without
-//     pairs. 6 us at that size.
+//     pairs. 7 us at that size.
 //
 // The tensor cores cut what they add to an fp32 accumulator towards zero, so a sum of 1024
 // terms in steps of 16 comes out up to 64 * 2^-24 smaller: d_weights, which is not rounded
@@ -1816,8 +1818,8 @@ cudaError_t pair_launch(const void* W, moe_dtype_t dtype, const PairArgs& a, int
 // Columns per tile: the width whose tiles take the SMs the least time. A tile of 64, 128 or
 // 256 columns takes about 10, 11 or 18 (the two halves of the wider ones drain at once, the
 // gather is the same), and the tiles go around in whole turns. Forward and backward, K = 2:
-// 5003 tokens, E 4, H 128: 64 columns 28.0 us, 128: 25.8; 4,000, E 8, H 256: 41.2 / 39.2,
-// 256: 41.1; 2,500, E 16, H 1024: 78.6 / 73.4 / 77.3; 30,000, E 8, H 256: 98.7 / 84.8 / 84.3.
+// 5003 tokens, E 4, H 128: 64 columns 37.7 us, 128: 35.4; 4,000, E 8, H 256: 50.8 / 48.5,
+// 256: 53.0; 2,500, E 16, H 1024: 115.6 / 105.8 / 111.9; 30,000, E 8, H 256: 142.9 / 129.9 / 133.0.
 int tile_columns(int64_t P, int E, int H, int sms) {
     const int64_t hit = P < E ? P : E, some = P / 128 + hit / 2, rows = some > hit ? some : hit;  // of 128 pairs, about
     auto time = [&](int bn, int each) { return (rows * ((H + bn - 1) / bn) + sms - 1) / sms * each; };
@@ -1838,10 +1840,12 @@ cudaError_t pair_width(const void* W, moe_dtype_t dtype, const PairArgs& a, int 
 
 template <typename T, bool DW>
 cudaError_t join_launch(const JoinArgs& a, int sms, cudaStream_t s) {
-    // the most lanes a token that work seven eighths of the time (H 192, K 3, 224,532 tokens: 8 lanes
-    // 76 us, 32 of which 24 work 112; H 832, K 3, 20,000 tokens: 8 lanes 41, 32 of which 26 work 36)
+    // the most lanes a token that work seven eighths of the time at two turns each. Product and join,
+    // forward / backward, 8, 16 and 32 lanes: H 192, K 3, 224,532 tokens: 262 / 356 us, 259 / 373,
+    // 282 / 429; H 128, K 4, 98,489: 96 / 126, 96 / 130, 99 / 149; H 1024, K 2, 16,384: 124 / 128,
+    // 105 / 127, 105 / 123
     int lpt = 32;
-    while (lpt > 8 && 8 * a.H < 7 * (lpt * 4) * ((a.H + lpt * 4 - 1) / (lpt * 4))) lpt /= 2;
+    while (lpt > 8 && 8 * a.H < 7 * (lpt * 8) * ((a.H + lpt * 8 - 1) / (lpt * 8))) lpt /= 2;
     auto go = [&](auto kernel, int u) {
         const int64_t tokens = 8 * (32 / lpt) * u, want = (a.T + tokens - 1) / tokens, cap = static_cast<int64_t>(sms) * 8;
         return launch_pdl(kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s, a, lpt);
@@ -1852,13 +1856,15 @@ cudaError_t join_launch(const JoinArgs& a, int sms, cudaStream_t s) {
     return go(join_kernel<T, 16, 1, DW>, 1);
 }
 
-// Whether the tokens are grouped by their two experts. Grouping takes about 13 us, and the
-// tiles of the E (E + 1) / 2 classes have to be mostly full. Forward, rows joined / grouped:
-// E 8, H 256: 36,864 tokens 30.9 / 34.3 us, 73,728: 55.6 / 40.5; E 16, H 128: 69,632 tokens
-// 31.1 / 34.9, 139,264: 56.1 / 45.5; forward and backward together cross at the same sizes.
+// Whether the tokens are grouped by their two experts. Grouping takes about 13 us, which the
+// waiting rows' traffic has to outweigh, and the tiles of the E (E + 1) / 2 classes must not be
+// mostly empty. Rows joined / grouped, forward + backward for d_x and d_weights: E 8, H 256:
+// 20,000 tokens 64 / 64 us, 24,576: 70 / 64, 73,728: 193 / 119; E 4, H 64: 65,536: 54 / 60, 98,304:
+// 82 / 74; E 24, H 64: 65,536: 56 / 69, 150,000: 132 / 108; E 16, H 128: 32,768: 52 / 64, 49,152:
+// 78 / 74; E 24, H 256: 30,000 (100 a class) 91 / 78; E 32, H 256: 50,000 (95 a class) 141 / 113.
 bool takes_duo(const int32_t* expert_idx, int64_t T_, int E, int K, int H) {
-    return K == 2 && expert_idx && aligned(expert_idx, 8) && H <= kDuoMaxH && E <= kDuoMaxE && T_ >= 49152 &&
-           T_ >= 640 * static_cast<int64_t>(E * (E + 1) / 2);
+    return K == 2 && expert_idx && aligned(expert_idx, 8) && H <= kDuoMaxH && E <= kDuoMaxE && T_ * H >= (6 << 20) &&
+           T_ >= 96 * static_cast<int64_t>(E * (E + 1) / 2);
 }
 
 template <typename T, bool DX>

@@ -25,9 +25,10 @@ inline int wgrad_tiles(int H) {
 // tiles, as many as fill the GPU once; with several tiles an expert, half as many experts as fill
 // it or more, and pairs enough, as many as fill it twice, since experts of uneven sizes would
 // leave the one turn to the largest; where the experts alone fill it, one is cut where its tiles
-// would take a block longer than an even share of all the work. K = 1 or 2, both kernels, filled
-// once / twice: 25,780 tokens, E 13, H 640: 87 / 64 us; 12,000, E 30, H 512 (648 pairs a piece):
-// 67 / 56; 2,000, E 8, H 1024 (444): 34 / 40; 6,000, E 13, H 640 (375): 35 / 43.
+// would take a block longer than an even share of all the work. dW, filled once / twice, uneven
+// experts: 25,780 tokens, K 1, E 13, H 640: 206 / 86 us; 12,000, K 2, E 30, H 512 (648 pairs a
+// piece): 72 / 62; 2,000, K 2, E 8, H 1024 (444): 37 / 45; 4,500, K 1, E 13, H 640 (281): 40 / 46.
+// Even experts lose by it (25,780 tokens: 64 / 86).
 inline int wgrad_extra(int64_t P, int E, int H) {
     const int tiles = wgrad_tiles(H), fill = kWUnits / tiles;
     if (E >= fill) return fill;

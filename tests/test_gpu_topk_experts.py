@@ -539,7 +539,7 @@ def test_two_experts_without_expert_indices(T):
 
 @pytest.mark.parametrize("T,E,K,H,dtype", [(40, 3, 2, 4096, BF16), (300, 2, 1, 4096, F16), (130, 2, 2, 2048, F16),
                                            (100000, 8, 1, 256, BF16), (60000, 8, 2, 256, F16), (20001, 12, 8, 128, BF16),
-                                           (9000, 20, 16, 64, F16)])
+                                           (9000, 20, 16, 64, F16), (100001, 3, 2, 64, BF16), (51001, 32, 2, 128, BF16)])
 def test_the_ends_of_the_range(T, E, K, H, dtype):
     """The widest rows, one expert for many tokens, many experts a token, fp16 in the grouped path."""
     x, W, b, g = _data(T, E, K, H, dtype)
