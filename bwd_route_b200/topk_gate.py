@@ -66,7 +66,8 @@ class MoETopKGate:
     def backward(self, x: torch.Tensor, gate_logits: torch.Tensor, d_y: torch.Tensor, accumulate_logits: bool = False,
                  stream=None):
         """After forward with the same x and gate_logits: d_x, d_logits, dW, db, dgamma and dbeta from
-        d_y [T, H]. accumulate_logits adds to d_logits (a balance loss's gradient, say)."""
+        d_y [T, H]. accumulate_logits adds to what self.d_logits holds (a balance loss's gradient that
+        was written there, say; nothing is there before the first call)."""
         ops.moe_topk_bwd(self.normed if self.norm else x, self.W, self.bias, d_y, self.routing, self.weights,
                          self.d_normed, self.dW, self.db, self.d_weights, self.ws, stream)
         ops.moe_topk_route_bwd(gate_logits, self.rule, self.routing.expert_idx, self.d_weights, self.d_logits,

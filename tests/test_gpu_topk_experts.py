@@ -558,3 +558,24 @@ def test_some_outputs_of_grouped_tokens(want):
     routing, w = _routing(T, E, K)
     o = _reference(x, W, b, g, routing.expert_idx, w)
     _check_bwd(_bwd(x, W, b, g, routing, w, want), o, routing, K, H, want)
+
+
+def test_a_captured_fp16_backward_follows_its_inputs():
+    """The powers of two that the terms of dW are staged with come from each call's own inputs."""
+    T, E, K, H = 700, 5, 2, 128
+    x, W, b, g = _data(T, E, K, H, F16)
+    routing, w = _routing(T, E, K)
+    ws = ops.new_topk_workspace(T, E, K, H, "cuda")
+    outs = {k: v.clone() for k, v in _bwd(x, W, b, g, routing, w, ws=ws).items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.moe_topk_bwd(x, W, b, g, routing, w, *(outs[k] for k in OUTS), ws)
+    first = g.clone()
+    for scale in (2.0 ** -12, 2.0 ** 8, 1.0):
+        g.copy_(first * scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = _bwd(x, W, b, g, routing, w)
+        assert all(torch.equal(outs[k], want[k]) for k in OUTS)
+        o = _reference(x, W, b, g, routing.expert_idx, w)
+        _check_dW(outs["dW"], o, routing)
