@@ -1306,7 +1306,8 @@ struct Unit {
 // Two 16-bit numbers that add up to s: the upper one is s cut off, always of a smaller
 // magnitude, the lower one the rest, rounded (16 bits of s for bf16, 22 for fp16). So both have
 // the sign of s, and an infinite x times either is the same infinity; an infinite s is infinite
-// in both. Masks rather than conversions back and forth: 124 us instead of 141 at the size above.
+// in both. Masks rather than conversions back and forth: 127 us instead of 141 for
+// dW alone at the size above, 110 without any of this arithmetic.
 template <typename T>
 __device__ __forceinline__ void split8(const float (&s)[8], uint4& hi, uint4& lo) {
     constexpr uint32_t kKeep = std::is_same<T, __half>::value ? 0xffffe000u : 0xffff0000u;

@@ -10,8 +10,9 @@
 //
 // Choices are exact. Without a bias the order of v is that of the logits, which are
 // compared as they are. With a bias (or sums of scores per group) v is computed in
-// fp32, and where two neighbours in the result lie within the error of that
-// computation the token is chosen again in fp64; about one in a thousand is.
+// fp32, and where two neighbours among the chosen, or the last of them and any other
+// expert, lie within the error of that computation and are no true tie the token is
+// chosen again in fp64; about one in a thousand is.
 //
 // A token belongs to LPT lanes with VPL consecutive experts each. Up to 64 experts a
 // warp works on 32 / LPT tokens at once: K rounds of a local maximum, a shuffle maximum
@@ -23,9 +24,10 @@
 //
 // What bounds it: the issue of instructions, about 650 a token of 256 experts with a bias
 // and groups (59 % of the issue slots used, 13 % of the DRAM bandwidth). 65,536 x 256 fp32,
-// 4 of 8 groups stay, K = 8: choice 66 us, scan 5.3, lists 10.0; rounds of a warp
+// 4 of 8 groups stay, K = 8: choice 67 us, scan 5.3, lists 10.0; rounds of a warp
 // maximum instead of the threshold took 130 us, fp64 for every open token on the spot 112.
-// 8 tokens x 64 experts: 6.5 us on the device, one chain of dependent steps.
+// 8 tokens x 64 experts: 6.9 us on the device, one chain of dependent steps. 262,144 x 8, K = 2:
+// 19 us by logits, 24 with a bias; 262,144 x 64, K = 6, with a bias: 132 us.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -902,8 +904,8 @@ topk_scatter_kernel(const int32_t* __restrict__ expert_idx, int64_t pairs, int p
 
 // Gradient of the logits: a token per LPT lanes, its row of gradients built in shared
 // memory (zeros and the K chosen entries) and written as a whole. 262,144 x 8 fp32, K = 2,
-// softmax: 6.4 us for 21 MB (3.3 TB/s, from L2 as a step finds it); 20,479 x 60 bf16, K = 4:
-// 6.1 us, a chain of three dependent loads.
+// softmax: 5.8 us for 21 MB (3.6 TB/s, from L2 as a step finds it); 20,479 x 60 bf16, K = 4:
+// 5.8 us, a chain of three dependent loads.
 //   renormalised: d l_k = w_k (g_k - sum_j w_j g_j) for the chosen, w summing to 1, times
 //   (1 - s_k) for the sigmoid; softmax: d l_e = s_e (g_e - sum_j s_j g_j), g = 0 for the
 //   others; sigmoid: g_k s_k (1 - s_k).  g: the weight's gradient times scale.

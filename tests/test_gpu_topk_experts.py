@@ -11,6 +11,8 @@ magnitude in it: A(n) = (n / 16 + 8) 2^-22 of the sum of the terms' magnitudes.
   term, so beyond 8 r sqrt(sum of squares) with probability below 2 exp(-32) per
   element (Hoeffding); A(n) of the magnitudes for n pairs, r of the result.
   db: n u of the magnitudes, r of the result.
+The 16-bit rows of y and d_x and the rounded terms of dW are an allowance: the tests of rows
+added in fp32 and of fp32 terms, further down, hold the calls to bounds without it.
 """
 import numpy as np
 import pytest
