@@ -1238,7 +1238,7 @@ struct WgradArgs {
 // fp16: w g is staged times a power of two per expert that brings the expert's largest finite
 // |w g| to [2^14, 2^15), and the sums are divided by it. Unscaled, a term above 65,504 would
 // be infinite and one below 6e-5 would lose its bits, though dW itself is in range. `peak`: the
-// bits of that largest value; the factor's exponent is kept in range, for peaks above 2^-113.
+// bits of that largest value; below 2^-112 the factor stays at 2^126, the largest that has an inverse.
 __device__ __forceinline__ int peak_exponent(uint32_t peak) { return max(static_cast<int>(peak >> 23), 15); }
 __device__ __forceinline__ float peak_factor(uint32_t peak) {
     return __uint_as_float(static_cast<uint32_t>(268 - peak_exponent(peak)) << 23);
@@ -1248,8 +1248,8 @@ __device__ __forceinline__ float peak_inverse(uint32_t peak) {
 }
 
 // peak[e] (zeroed): bits of the largest finite |w g| over the pairs of expert e. A warp takes
-// eight slots of perm, a lane each, reads their rows of g and leaves one maximum per expert. Bound by L2: K reads
-// of g. fp16 only; 16,384 tokens, K 2, H 1024: 16 us.
+// eight slots of perm, a lane each, reads their rows of g and leaves one maximum per expert.
+// Bound by L2: K reads of g. fp16 only; 16,384 tokens, K 2, H 1024: 16 us.
 constexpr int kPeakSlots = 8;  // of a warp at a time: 32 of them leave most of the GPU idle (38 us)
 __global__ void __launch_bounds__(256) wgrad_peak_kernel(const WgradArgs A) {
     griddep_wait();  // every global access below comes after the previous grid
@@ -1304,9 +1304,9 @@ struct Unit {
 };
 
 // Two 16-bit numbers that add up to s: the upper one is s cut off, always of a smaller
-// magnitude, the lower one the rest, rounded (16 bits of s for bf16, 22 for fp16). So both have
-// the sign of s, and an infinite x times either is the same infinity; an infinite s is infinite
-// in both. Masks rather than conversions back and forth: 127 us instead of 141 for
+// magnitude, the lower one the rest, rounded (16 bits of s for bf16; 22 for fp16, down to its
+// last step, 2^-39 of the expert's largest). So both have the sign of s, and an infinite x times
+// either is the same infinity; an infinite s is infinite in both. Masks rather than conversions back and forth: 127 us instead of 141 for
 // dW alone at the size above, 110 without any of this arithmetic.
 template <typename T>
 __device__ __forceinline__ void split8(const float (&s)[8], uint4& hi, uint4& lo) {
